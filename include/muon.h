@@ -220,6 +220,86 @@ int muon_adamw_untie(const float* param, const float* exp_avg, const float* exp_
                      float* new_exp_avg, float* new_exp_avg_sq, int64_t rows, int64_t cols, int transpose,
                      hipStream_t stream);
 
+/*
+ * Global gradient norm and clipping ("Let's reproduce GPT-2 (124M)" clips the
+ * global norm at 1.0 before every optimizer step).  Over every element of
+ * every tensor of the call, with g the gradients:
+ *   norm   = scale * sqrt(sum of g^2)
+ *   c      = min(1, max_norm / (norm + 1e-6)), 1 when max_norm = inf
+ *   factor = scale * c
+ * and the clipped gradient is g' = fp32(fp32(g) * factor), one rounding.  The
+ * sum is held in fp64 in a fixed order, so equal calls give equal bits; norm
+ * and factor are each rounded once, to fp32.  `scale` serves gradient
+ * accumulation (1 / micro-batches) and loss scaling (1 / loss scale).
+ * An infinity among the gradients gives norm = inf and factor = 0 (under a
+ * finite max_norm), a NaN gives NaN for both; a norm beyond the fp32 range
+ * reads as inf.
+ *
+ * The result is a record of MUON_CLIP_RECORD_FLOATS floats on the device,
+ * {norm, factor}.  Steps on clipped gradients (muon_step_clip,
+ * muon_adamw_step_clip) read it there, so the gradients are never written
+ * back and the host never waits.  A step whose record's norm is not finite
+ * changes nothing: parameters, momentum and moments keep their bits.
+ *
+ * Arguments shared by the calls below:
+ *   dtypes      host array: element type of each tensor, MUON_FP32, MUON_BF16
+ *               or MUON_FP16, mixed as needed
+ *   numels      host array: contiguous elements of each tensor, 0 .. 2^35; a
+ *               tensor with 0 elements takes no part (its pointer may be NULL)
+ *   n           0 .. MUON_GRAD_MAX_TENSORS; with no elements at all the norm is 0
+ *   max_norm    >= 0, or inf;  scale finite, > 0
+ *   record      device, MUON_CLIP_RECORD_FLOATS floats, 4-byte aligned
+ *   workspace   device, MUON_GRAD_WORKSPACE_BYTES bytes, 16-byte aligned, all
+ *               zero before its first use; a call that finishes leaves it ready for the
+ *               next.  Calls that share a workspace must be ordered on the GPU;
+ *               calls with workspaces and records of their own may overlap.
+ * Tensors are aligned to their element type only.  These calls use none of
+ * the library's workspace or plan tables: they allocate nothing, cache
+ * nothing, and can be captured without an earlier call.
+ */
+#define MUON_FP32 0
+#define MUON_BF16 1
+#define MUON_FP16 2
+#define MUON_GRAD_MAX_TENSORS 65536
+#define MUON_CLIP_RECORD_FLOATS 2
+#define MUON_GRAD_WORKSPACE_BYTES 16640
+
+/* The record of the gradients' norm.  Gradients are read only, and may share
+ * memory with one another (each is counted). */
+int muon_grad_norm(const void* const* grads, const int64_t* numels, const int* dtypes, int n, float max_norm,
+                   float scale, float* record, void* workspace, hipStream_t stream);
+
+/*
+ * The record, and the clipped gradients g' rounded once (nearest even) to
+ * out_dtypes[i] in outs[i]: other tensors, of the gradients' types or not
+ * (16-bit gradients into fp32 ones), or the gradients themselves
+ * (outs[i] = grads[i], same type).  In place a factor of 1 writes nothing.
+ * No out may overlap another array of the call.
+ */
+int muon_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                   const int* out_dtypes, int n, float max_norm, float scale, float* record, void* workspace,
+                   hipStream_t stream);
+
+/*
+ * muon_adamw_step on the clipped gradients g' of the record, which may be of
+ * 16-bit types.  Same arithmetic on g', same argument rules, no cached work
+ * list; record may be NULL (factor 1: on fp32 gradients, muon_adamw_step's
+ * bits).  The gradients may share memory with one another.
+ */
+int muon_adamw_step_clip(float* const* params, const void* const* grads, const int* grad_dtypes,
+                         float* const* exp_avg, float* const* exp_avg_sq, const int64_t* numels,
+                         const float* weight_decay, int n, float lr, float beta1, float beta2, float eps,
+                         int64_t step, const float* record, hipStream_t stream);
+
+/*
+ * muon_step_sched (3 * ns_steps coefficients) on the clipped gradients g' of
+ * the record; record may be NULL (factor 1: muon_step_sched's bits).  Under a
+ * norm that is not finite `updates` receives zeros.
+ */
+int muon_step_clip(float* const* params, const float* const* grads, float* const* momentum,
+                   const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps, const float* coeffs,
+                   uint16_t* const* updates, const float* record, hipStream_t stream);
+
 /* Thread-local description of the last failing call on this thread ("" if none). */
 const char* muon_last_error(void);
 
@@ -281,7 +361,9 @@ int muon_set_lanes(int lanes);
 #define MUON_KERNEL_POLY 3     /* B = b A + c A A */
 #define MUON_KERNEL_UPDATE 4   /* X <- a X + B X */
 #define MUON_KERNEL_APPLY 5    /* W -= lr X */
-#define MUON_KERNEL_ADAMW 6    /* multi-tensor AdamW (muon_adamw_step) */
+#define MUON_KERNEL_ADAMW 6    /* multi-tensor AdamW (muon_adamw_step, muon_adamw_step_clip) */
+#define MUON_KERNEL_GRAD_NORM 7 /* global gradient norm */
+#define MUON_KERNEL_GRAD_CLIP 8 /* clipped gradients of muon_grad_clip */
 int muon_timing_enable(int kernel);
 int muon_timing_read(double* total_ms, int64_t* launches);
 

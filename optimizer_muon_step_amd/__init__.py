@@ -3,25 +3,30 @@
 Thin argument marshalling over the C ABI declared in include/muon.h; every
 step of the computation runs in the library's HIP kernels.  Tensors are torch
 tensors on the current HIP device: fp32 params/grads/momentum, bf16 for the
-Newton-Schulz entry.  Calls enqueue on torch's current stream (or `stream`)
+Newton-Schulz entry; the gradients of the norm, clip and AdamW calls may be
+bf16 or fp16 too.  Calls enqueue on torch's current stream (or `stream`)
 and return without synchronising.
 """
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 from . import _lib
 
 __all__ = [
     "DEFAULT_COEFFS", "MuonError", "matrix_shape", "muon_step", "muon_step_noalloc", "muon_newton_schulz", "muon_adamw_step", "muon_adamw_untie",
+    "muon_grad_norm", "muon_grad_clip",
     "muon_workspace_bytes",
     "muon_set_workspace", "muon_release", "muon_plan_stats", "muon_set_lanes", "muon_timing_enable", "muon_timing_read", "muon_last_error",
     "KERNEL_MOMENTUM", "KERNEL_CAST", "KERNEL_GRAM", "KERNEL_POLY", "KERNEL_UPDATE", "KERNEL_APPLY",
-    "KERNEL_ADAMW",
+    "KERNEL_ADAMW", "KERNEL_GRAD_NORM", "KERNEL_GRAD_CLIP",
 ]
 
 DEFAULT_COEFFS = (3.4445, -4.7750, 2.0315)
 KERNEL_MOMENTUM, KERNEL_CAST, KERNEL_GRAM, KERNEL_POLY, KERNEL_UPDATE, KERNEL_APPLY, KERNEL_ADAMW = range(7)
+KERNEL_GRAD_NORM, KERNEL_GRAD_CLIP = 7, 8
+GRAD_WORKSPACE_BYTES = 16640
 _CODES = {-1: "MUON_EINVAL", -2: "MUON_ENOMEM", -3: "MUON_EHIP"}
 
 
@@ -95,13 +100,32 @@ def _coeff_arg(coeffs, ns_steps):
     return True, _lib.float_array([float(v) for r in rows for v in r])
 
 
+def _update_ptrs(updates, params):
+    if updates is None:
+        return None
+    if len(updates) != len(params):
+        raise ValueError("updates must have one entry per matrix")
+    ptrs = []
+    for i, u in enumerate(updates):
+        if u is None:
+            ptrs.append(None)
+            continue
+        _bf16_matrix(u, f"updates[{i}]")
+        if u.shape != params[i].shape:
+            raise ValueError(f"updates[{i}]: shape differs from params[{i}]")
+        ptrs.append(u.data_ptr())
+    return _lib.ptr_array(ptrs)
+
+
 def muon_step(params, grads, momentum, lr=0.02, beta=0.95, ns_steps=5, coeffs=DEFAULT_COEFFS,
-              updates=None, stream=None) -> None:
+              updates=None, stream=None, clip=None) -> None:
     """One Muon step over lists of fp32 tensors of rank >= 2 (params and
     momentum updated in place; rank > 2 is taken as the matrix_shape view).
     `coeffs` is one (a, b, c) or a schedule of ns_steps triples.  `updates`, if
     given, is a list of bf16 tensors (or None entries) of the params' shapes
-    receiving the applied update."""
+    receiving the applied update.  `clip`, if given, is the record of
+    muon_grad_norm: the step then takes the gradients clipped, and changes
+    nothing when the record's norm is not finite."""
     n = len(params)
     if len(grads) != n or len(momentum) != n:
         raise ValueError("params, grads and momentum must have the same length")
@@ -118,24 +142,19 @@ def muon_step(params, grads, momentum, lr=0.02, beta=0.95, ns_steps=5, coeffs=DE
     S = _lib.shape_array(shapes)
     sched, C = _coeff_arg(coeffs, ns_steps)
     st = ctypes.c_void_p(_stream_handle(stream))
-    if updates is None:
+    if clip is not None:
+        record = _record_ptr(clip)
+        if not sched:  # the same triple every iteration (a count out of range is the library's to refuse)
+            C = _lib.float_array(list(C) * min(max(int(ns_steps), 0), 65))
+        rc = lib.muon_step_clip(P, G, M, S, n, float(lr), float(beta), int(ns_steps), C, _update_ptrs(updates, params),
+                                record, st)
+    elif updates is None:
         if sched:
             rc = lib.muon_step_sched(P, G, M, S, n, float(lr), float(beta), int(ns_steps), C, None, st)
         else:
             rc = lib.muon_step(P, G, M, S, n, float(lr), float(beta), int(ns_steps), C, st)
     else:
-        if len(updates) != n:
-            raise ValueError("updates must have one entry per matrix")
-        ptrs = []
-        for i, u in enumerate(updates):
-            if u is None:
-                ptrs.append(None)
-                continue
-            _bf16_matrix(u, f"updates[{i}]")
-            if u.shape != params[i].shape:
-                raise ValueError(f"updates[{i}]: shape differs from params[{i}]")
-            ptrs.append(u.data_ptr())
-        U = _lib.ptr_array(ptrs)
+        U = _update_ptrs(updates, params)
         entry = lib.muon_step_sched if sched else lib.muon_step_ex
         rc = entry(P, G, M, S, n, float(lr), float(beta), int(ns_steps), C, U, st)
     _check(rc)
@@ -195,11 +214,118 @@ def _fp32_flat(t, what):
     return t.data_ptr()
 
 
+def _any_16_bit(ts):
+    import torch
+    halves = (torch.bfloat16, torch.float16)
+    return any(getattr(t, "dtype", None) in halves for t in ts)
+
+
+def _dense(t):
+    """Whether t's elements fill one stretch of memory, each once, in any order of dimensions."""
+    want = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+_TYPE_CODES = {}
+
+
+def _flat_list(ts, what, any_type, dense):
+    """(addresses, element counts, type codes) of a list of tensors taken flat, as C arrays."""
+    import torch
+    if not _TYPE_CODES:
+        _TYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    dev = None
+    ptrs, numels, types = array("Q"), array("q"), array("i")
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{what}[{i}]: expected a tensor")
+        code = _TYPE_CODES.get(t.dtype, -1)
+        if code < 0 or (code > 0 and not any_type):
+            raise ValueError(f"{what}[{i}]: expected {'float32, bfloat16 or float16' if any_type else 'float32'}, "
+                             f"not {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{what}[{i}]: expected a tensor on the GPU")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{what}[{i}] is on GPU {t.get_device()}, the current one is {dev}")
+        if not (t.is_contiguous() or (dense and _dense(t))):
+            raise ValueError(f"{what}[{i}]: expected a {'dense' if dense else 'contiguous'} tensor")
+        ptrs.append(t.data_ptr())
+        numels.append(t.numel())
+        types.append(code)
+    return ptrs, numels, types
+
+
+def _address(a):
+    return a.buffer_info()[0]
+
+
+def _record_ptr(record):
+    import torch
+    if (not isinstance(record, torch.Tensor) or record.dtype != torch.float32 or record.numel() != 2
+            or not record.is_contiguous() or record.get_device() != torch.cuda.current_device()):
+        raise ValueError("record: expected the contiguous float32 tensor of 2 of muon_grad_norm, on the current GPU")
+    return record.data_ptr()
+
+
+class _NoStream:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return None
+
+
+def _on_stream(stream):
+    """A context in which `stream` is torch's current one, so that what a call
+    allocates belongs to the stream that uses it."""
+    if stream is None:
+        return _NoStream()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+# One norm workspace per device and stream: calls on one stream are ordered,
+# so each finds it as the one before left it; calls on two streams share none.
+_norm_workspaces = {}
+
+
+def _norm_buffers(record):
+    """(record, workspace, stream handle) of a norm on torch's current stream.
+    A captured call takes a workspace of its own from the graph's memory,
+    cleared by the graph, so that graphs share none either."""
+    import torch
+    st = torch.cuda.current_stream()
+    handle, dev = st.cuda_stream, st.device
+    if record is None:
+        record = torch.empty(2, dtype=torch.float32, device=dev)
+    else:
+        _record_ptr(record)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
+        ws[:8].zero_()
+        return record, ws, handle
+    ws = _norm_workspaces.get((dev.index, handle))
+    if ws is None:
+        ws = _norm_workspaces[dev.index, handle] = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
+    return record, ws, handle
+
+
 def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
-                    step=1, stream=None) -> None:
+                    step=1, stream=None, clip=None) -> None:
     """One AdamW step over tensors of any shape (each contiguous fp32, taken
-    flat); exp_avg and exp_avg_sq start at zero and `step` counts from 1.
-    `weight_decay` is one value or one per tensor."""
+    flat; the gradients may be bf16 or fp16); exp_avg and exp_avg_sq start at
+    zero and `step` counts from 1.  `weight_decay` is one value or one per
+    tensor.  `clip`, if given, is the record of muon_grad_norm: the step then
+    takes the gradients clipped, and changes nothing when the record's norm is
+    not finite."""
     n = len(params)
     if not (len(grads) == len(exp_avg) == len(exp_avg_sq) == n):
         raise ValueError("params, grads, exp_avg and exp_avg_sq must have the same length")
@@ -209,6 +335,8 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
             raise ValueError("weight_decay: expected one value or one per tensor")
     else:
         wds = [float(weight_decay)] * n
+    if clip is not None or _any_16_bit(grads):
+        return _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip)
     ptrs = ([], [], [], [])
     numels = []
     for i in range(n):
@@ -224,6 +352,64 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
                                      _lib.float_array(wds), n, float(lr), float(b1), float(b2), float(eps),
                                      int(step), ctypes.c_void_p(_stream_handle(stream)))
     _check(rc)
+
+
+def _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip):
+    lists = [_flat_list(ts, what, any_type=what == "grads", dense=False)
+             for ts, what in ((params, "params"), (grads, "grads"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"))]
+    (p, numels, _), (g, g_numels, types), (u, u_numels, _), (v, v_numels, _) = lists
+    if not numels == g_numels == u_numels == v_numels:
+        i = next(i for i in range(len(numels)) if len({a[i] for a in (numels, g_numels, u_numels, v_numels)}) != 1)
+        raise ValueError(f"tensor {i}: element counts differ")
+    record = None if clip is None else _record_ptr(clip)
+    _check(_lib.load().muon_adamw_step_clip(_address(p), _address(g), _address(types), _address(u), _address(v),
+                                            _address(numels), _lib.float_array(wds), len(p), float(lr),
+                                            float(betas[0]), float(betas[1]), float(eps), int(step), record,
+                                            _stream_handle(stream)))
+
+
+def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=None):
+    """The global norm of a list of gradients and the factor that clips it:
+    a float32 tensor {norm, factor} on the GPU with
+        norm = scale * sqrt(sum of g^2),  factor = scale * min(1, max_norm / (norm + 1e-6)).
+    Gradients are float32, bfloat16 or float16, mixed as needed, each dense in
+    memory (any order of dimensions).  `scale` is 1 / micro-batches under
+    gradient accumulation, 1 / loss scale under loss scaling.  Pass the result
+    as `clip` to muon_step and muon_adamw_step, which then take the gradients
+    clipped without a pass that writes them back.  `record` is a tensor of 2
+    to fill instead of a new one."""
+    ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
+    lib = _lib.load()
+    with _on_stream(stream):
+        record, ws, st = _norm_buffers(record)
+        _check(lib.muon_grad_norm(_address(ptrs), _address(numels), _address(types), len(ptrs), float(max_norm),
+                                  float(scale), record.data_ptr(), ws.data_ptr(), st))
+    return record
+
+
+def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=None):
+    """Clip a list of gradients by their global norm: every gradient times the
+    factor of muon_grad_norm, in place, or rounded into `outs`, tensors of the
+    same shapes and memory order and of any of the three types (16-bit
+    gradients into float32 ones, say).  Returns the record {norm, factor};
+    the norm is the one before clipping."""
+    ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
+    if outs is None:
+        out_ptrs, out_types = ptrs, types
+    else:
+        if len(outs) != len(ptrs):
+            raise ValueError("grads and outs must have the same length")
+        out_ptrs, _, out_types = _flat_list(outs, "outs", any_type=True, dense=True)
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if g.shape != o.shape or (g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous())):
+                raise ValueError(f"outs[{i}]: shape or memory order differs from grads[{i}]")
+    lib = _lib.load()
+    with _on_stream(stream):
+        record, ws, st = _norm_buffers(record)
+        _check(lib.muon_grad_clip(_address(ptrs), _address(out_ptrs), _address(numels), _address(types),
+                                  _address(out_types), len(ptrs), float(max_norm), float(scale), record.data_ptr(),
+                                  ws.data_ptr(), st))
+    return record
 
 
 def muon_adamw_untie(param, exp_avg, exp_avg_sq, transpose=False, stream=None):
@@ -260,6 +446,7 @@ def muon_set_workspace(ptr: int | None, nbytes: int = 0) -> None:
 
 def muon_release() -> None:
     _lib.load().muon_release()
+    _norm_workspaces.clear()
 
 
 PLAN_STATS = ("plan_builds", "uploads", "pointer_patches", "device_syncs", "evictions", "workspace_allocs")

@@ -34,6 +34,12 @@ SIGNATURES = {
                                        ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                        ctypes.c_int64, _P]),
     "muon_adamw_untie": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _P]),
+    "muon_grad_norm": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
+    "muon_grad_clip": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
+    "muon_adamw_step_clip": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _FLOAT3, ctypes.c_int, ctypes.c_float,
+                                            ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_int64, _P, _P]),
+    "muon_step_clip": (ctypes.c_int, [_PP, _PP, _PP, _SHAPES, ctypes.c_int, ctypes.c_float, ctypes.c_float,
+                                      ctypes.c_int, _FLOAT3, _PP, _P, _P]),
     "muon_last_error": (ctypes.c_char_p, []),
     "muon_workspace_bytes": (ctypes.c_size_t, [_SHAPES, ctypes.c_int]),
     "muon_set_workspace": (ctypes.c_int, [_P, ctypes.c_size_t]),

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "muon_internal.h"
@@ -13,8 +14,50 @@
 
 namespace muon {
 
+// Body of a C entry point: host allocation failure becomes MUON_ENOMEM, and no
+// exception leaves the library.
+template <typename F>
+int c_entry(F&& body) noexcept {
+  try {
+    return body();
+  } catch (const std::bad_alloc&) {
+    return fail(MUON_ENOMEM, "host memory allocation failed");
+  } catch (...) {
+    return fail(MUON_EINVAL, "internal error");
+  }
+}
+
 int fail_hip(hipError_t e, const char* what);
 int capture_status(hipStream_t stream, bool* capturing);
+
+// Timing of one kernel family (muon_timing_enable): its HIP events, as start
+// and end pairs.
+extern int g_time_kind;
+extern std::vector<hipEvent_t> g_ev;
+extern size_t g_ev_used;
+
+// Launch wrapper: brackets the launch with events when its family is timed.
+template <typename F>
+int timed(int kind, hipStream_t stream, F&& launch, const char* what) {
+  const bool on = (g_time_kind == kind);
+  hipError_t e;
+  if (on) {
+    if (g_ev_used + 2 > g_ev.size()) {
+      for (int k = 0; k < 2; ++k) {
+        hipEvent_t ev;
+        if ((e = hipEventCreate(&ev)) != hipSuccess) return fail_hip(e, "hipEventCreate");
+        g_ev.push_back(ev);
+      }
+    }
+    if ((e = hipEventRecord(g_ev[g_ev_used], stream)) != hipSuccess) return fail_hip(e, "hipEventRecord");
+  }
+  if ((e = launch()) != hipSuccess) return fail_hip(e, what);
+  if (on) {
+    if ((e = hipEventRecord(g_ev[g_ev_used + 1], stream)) != hipSuccess) return fail_hip(e, "hipEventRecord");
+    g_ev_used += 2;
+  }
+  return MUON_OK;
+}
 
 // Serialises every entry point's use of the library's host state.
 std::mutex& api_mutex();
@@ -40,7 +83,8 @@ Tables tables_at(char* block, const PlanTables& t, int lane, char* ws);
 int patch_records(MatDesc* desc, const std::vector<PtrRecord>& recs, hipStream_t stream);
 
 // The kernel sequence of one lane of a call (the caller holds api_mutex()).
+// record: {norm, factor} on the device for a step on clipped gradients, or null.
 int launch_sequence(int mode, const Tables& v, float lr, float beta, int ns_steps, const float* coeffs, int stride,
-                    hipStream_t stream);
+                    const float* record, hipStream_t stream);
 
 }  // namespace muon

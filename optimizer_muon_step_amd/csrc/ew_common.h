@@ -2,6 +2,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "muon_internal.h"
@@ -20,6 +21,19 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // pass (for the norm) and the cast pass (for X0) both take U from here.
 __device__ __forceinline__ float nesterov(float g, float m_new, float beta) {
   return g + beta * m_new;
+}
+
+// A step on clipped gradients reads g' = fp32(g * factor), factor from the
+// call's record {norm, factor}; a norm that is not finite leaves every
+// parameter and momentum buffer as it was.
+struct Clip {
+  float factor;
+  bool skip;
+};
+template <bool CLIP>
+__device__ __forceinline__ Clip clip_of(const float* __restrict__ record) {
+  if (!CLIP) return {1.0f, false};
+  return {record[1], !isfinite(record[0])};
 }
 
 // Block barrier that waits for this wave's LDS operations only, so global

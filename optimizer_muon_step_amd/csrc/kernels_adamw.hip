@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include "bf16_util.h"
+#include "grad_io.h"
 #include "muon_internal.h"
 
 namespace muon {
@@ -34,8 +35,8 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ void adamw_elem(float& p, float g, float& u, float& v, const AdamConst& c,
-                                           float decay) {
+template <typename Const>
+__device__ __forceinline__ void adamw_elem(float& p, float g, float& u, float& v, const Const& c, float decay) {
   const float p1 = p * decay;
   const float u1 = c.beta1 * u + c.omb1 * g;
   const float v1 = c.beta2 * v + (c.omb2 * g) * g;
@@ -99,6 +100,86 @@ __global__ __launch_bounds__(EW_THREADS) void adamw_kernel(const AdamDesc* __res
       Q[e] = ve;
     }
   }
+}
+
+namespace {
+
+// One chunk of len elements on gradients of type TG: g' = fp32(g) * factor,
+// one rounding, then adamw_elem.
+template <int TG>
+__device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, int64_t off, int len, float factor,
+                                                 float decay) {
+  typedef grad::Elem<TG> E;
+  typedef grad::f32x4_u vec;
+  constexpr int V = ADAMC_CHUNK / (4 * GRAD_THREADS);
+  MUON_GLOBAL float* P = gptr(a.p[t]) + off;
+  const MUON_GLOBAL typename E::scalar* G = gptr(static_cast<const typename E::scalar*>(a.g[t])) + off;
+  MUON_GLOBAL float* U = gptr(a.u[t]) + off;
+  MUON_GLOBAL float* Q = gptr(a.v[t]) + off;
+  if (len == ADAMC_CHUNK) {
+    MUON_GLOBAL vec* p4 = reinterpret_cast<MUON_GLOBAL vec*>(P);
+    const MUON_GLOBAL typename E::vec* g4 = reinterpret_cast<const MUON_GLOBAL typename E::vec*>(G);
+    MUON_GLOBAL vec* u4 = reinterpret_cast<MUON_GLOBAL vec*>(U);
+    MUON_GLOBAL vec* v4 = reinterpret_cast<MUON_GLOBAL vec*>(Q);
+    vec p[V], u[V], v[V];
+    typename E::vec gw[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) gw[k] = __builtin_nontemporal_load(&g4[k * GRAD_THREADS + threadIdx.x]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[k] = __builtin_nontemporal_load(&u4[k * GRAD_THREADS + threadIdx.x]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = __builtin_nontemporal_load(&v4[k * GRAD_THREADS + threadIdx.x]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) p[k] = __builtin_nontemporal_load(&p4[k * GRAD_THREADS + threadIdx.x]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const f32x4 g = E::widen(gw[k]) * factor;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float pe = p[k][e], ue = u[k][e], ve = v[k][e];
+        adamw_elem(pe, g[e], ue, ve, a, decay);
+        p[k][e] = pe;
+        u[k][e] = ue;
+        v[k][e] = ve;
+      }
+      __builtin_nontemporal_store(u[k], &u4[k * GRAD_THREADS + threadIdx.x]);
+      __builtin_nontemporal_store(v[k], &v4[k * GRAD_THREADS + threadIdx.x]);
+      __builtin_nontemporal_store(p[k], &p4[k * GRAD_THREADS + threadIdx.x]);
+    }
+  } else {
+    for (int e = threadIdx.x; e < len; e += GRAD_THREADS) {
+      float pe = P[e], ue = U[e], ve = Q[e];
+      adamw_elem(pe, E::widen1(G[e]) * factor, ue, ve, a, decay);
+      P[e] = pe;
+      U[e] = ue;
+      Q[e] = ve;
+    }
+  }
+}
+
+}  // namespace
+
+// The AdamW step on clipped gradients: the factor is read from the record on
+// the device.  A norm that is not finite leaves everything as it was.
+__global__ __launch_bounds__(GRAD_THREADS) void adamw_clip_kernel(const AdamClipArgs a) {
+  float factor = 1.0f;
+  if (a.record) {
+    factor = a.record[1];
+    if (!isfinite(a.record[0])) return;
+  }
+  const int it = blockIdx.x;
+  const int t = grad::find_tensor(a.start, 0, a.n, it);
+  const uint32_t tail = a.tail[t];
+  const int64_t off = (int64_t)(it - a.start[t]) * ADAMC_CHUNK;
+  const int len = it + 1 == a.start[t + 1] ? (int)(tail >> 4) : ADAMC_CHUNK;
+  const float decay = 1.0f - a.lr * a.wd[(tail >> 2) & 3];
+  grad::with_type(tail & 3, [&](auto tg) { adamw_clip_chunk<decltype(tg)::value>(a, t, off, len, factor, decay); });
+}
+
+hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s) {
+  if (a.items == 0) return hipSuccess;
+  adamw_clip_kernel<<<a.items, GRAD_THREADS, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 // Delayed untying: copy a shared parameter and its two AdamW moments into

@@ -60,10 +60,11 @@ __device__ __forceinline__ f32x4 load4_edge(const MUON_GLOBAL float* a, const Ma
 // through LDS for a transposed one.  G and M go out first, eight 16-byte
 // loads per thread in one batch on interior tiles, and the norm scale is
 // taken while they are in flight.
-template <bool FROM_BF16>
+// CLIP: on clipped gradients (clip_of); a skipped step gets X0 = 0.
+template <bool FROM_BF16, bool CLIP>
 __global__ __launch_bounds__(EW_THREADS) void cast_kernel(const MatDesc* __restrict__ descs,
                                                           const EwItem* __restrict__ items,
-                                                          float beta) {
+                                                          float beta, const float* __restrict__ record) {
   __shared__ float T[CAST_TILE][CAST_TILE + 1];
   const EwItem it = items[ew_item_of_block(blockIdx.x, gridDim.x, EW_TILE_RUN)];
   const MatDesc& d = descs[it.mat];
@@ -122,9 +123,11 @@ __global__ __launch_bounds__(EW_THREADS) void cast_kernel(const MatDesc* __restr
     } else {
       s = *d.scale;
     }
+    const Clip clip = clip_of<CLIP>(record);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const bool row_in = sr0 + tr + rstep * q < d.rows;
+      const bool row_in = sr0 + tr + rstep * q < d.rows && !clip.skip;
+      if (CLIP) g4[q] *= clip.factor;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         v[q][k] = (row_in && sc0 + tc + k < d.cols) ? nesterov(g4[q][k], m4[q][k], beta) * s : 0.0f;
@@ -165,9 +168,12 @@ __global__ __launch_bounds__(EW_THREADS) void cast_kernel(const MatDesc* __restr
 // EW_TILE_RUN, as in the cast): CAST_WIDE_ROWS x CAST_WIDE_COLS for an
 // untransposed matrix, CAST_TILE x CAST_TILE (X staged through LDS) for a
 // transposed one.
+// CLIP: a skipped step (clip_of) leaves W as it was.
+template <bool CLIP>
 __global__ __launch_bounds__(EW_THREADS) void apply_kernel(const MatDesc* __restrict__ descs,
                                                            const EwItem* __restrict__ items, float lr,
-                                                           int src, int write_w) {
+                                                           int src, int write_w,
+                                                           const float* __restrict__ record) {
   __shared__ uint16_t T[CAST_TILE][CAST_TILE + 2];
   const EwItem it = items[ew_item_of_block(blockIdx.x, gridDim.x, EW_TILE_RUN)];
   const MatDesc& d = descs[it.mat];
@@ -216,7 +222,7 @@ __global__ __launch_bounds__(EW_THREADS) void apply_kernel(const MatDesc* __rest
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[q][k] = T[tc + k][tr + 16 * q];
   }
-  if (write_w) {
+  if (write_w && !clip_of<CLIP>(record).skip) {
     MUON_GLOBAL float* W = gptr(d.W);
     const bool vec = d.vec4 && (c0 + tc + 3 < d.cols);
     // W is read and written once per step: non-temporal accesses
@@ -267,19 +273,24 @@ __global__ __launch_bounds__(EW_THREADS) void apply_kernel(const MatDesc* __rest
 }
 
 hipError_t launch_cast(const MatDesc* d, const EwItem* items, int n_items, float beta, int from_bf16,
-                       hipStream_t s) {
+                       const float* record, hipStream_t s) {
   if (n_items == 0) return hipSuccess;
   if (from_bf16)
-    cast_kernel<true><<<n_items, EW_THREADS, 0, s>>>(d, items, beta);
+    cast_kernel<true, false><<<n_items, EW_THREADS, 0, s>>>(d, items, beta, nullptr);
+  else if (record)
+    cast_kernel<false, true><<<n_items, EW_THREADS, 0, s>>>(d, items, beta, record);
   else
-    cast_kernel<false><<<n_items, EW_THREADS, 0, s>>>(d, items, beta);
+    cast_kernel<false, false><<<n_items, EW_THREADS, 0, s>>>(d, items, beta, nullptr);
   return hipGetLastError();
 }
 
 hipError_t launch_apply(const MatDesc* d, const EwItem* items, int n_items, float lr, int src,
-                        int write_w, hipStream_t s) {
+                        int write_w, const float* record, hipStream_t s) {
   if (n_items == 0) return hipSuccess;
-  apply_kernel<<<n_items, EW_THREADS, 0, s>>>(d, items, lr, src, write_w);
+  if (record)
+    apply_kernel<true><<<n_items, EW_THREADS, 0, s>>>(d, items, lr, src, write_w, record);
+  else
+    apply_kernel<false><<<n_items, EW_THREADS, 0, s>>>(d, items, lr, src, write_w, nullptr);
   return hipGetLastError();
 }
 

@@ -31,9 +31,12 @@ using namespace ew;
 // ones).  The new M is stored normally: the cast pass reads it again right
 // after, and part of it is still in the memory-side cache then (cast 136
 // against 149 us, momentum 170 against 168).
+// CLIP: on clipped gradients (clip_of); a skipped step leaves M as it was and
+// a partial of 0.
+template <bool CLIP>
 __global__ __launch_bounds__(EW_THREADS) void momentum_kernel(const MatDesc* __restrict__ descs,
                                                               const EwItem* __restrict__ items,
-                                                              float beta) {
+                                                              float beta, const float* __restrict__ record) {
   constexpr int V = MOM_CHUNK / (4 * EW_THREADS);  // float4 per thread
   __shared__ double red[kWaves];
   const EwItem it = items[ew_item_of_block(blockIdx.x, gridDim.x, EW_MOM_RUN)];
@@ -41,6 +44,11 @@ __global__ __launch_bounds__(EW_THREADS) void momentum_kernel(const MatDesc* __r
   const int64_t total = (int64_t)d.rows * d.cols;
   const int64_t base = (int64_t)it.idx * MOM_CHUNK;
   const int64_t end = min(base + (int64_t)MOM_CHUNK, total);
+  const Clip clip = clip_of<CLIP>(record);
+  if (CLIP && clip.skip) {
+    if (threadIdx.x == 0) d.part[it.idx] = 0.0;
+    return;
+  }
   const MUON_GLOBAL float* G = gptr(d.G);
   MUON_GLOBAL float* M = gptr(d.M);
   double ss = 0.0;
@@ -54,6 +62,7 @@ __global__ __launch_bounds__(EW_THREADS) void momentum_kernel(const MatDesc* __r
     for (int v = 0; v < V; ++v) m[v] = __builtin_nontemporal_load(&m4[v * EW_THREADS + threadIdx.x]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      if (CLIP) g[v] *= clip.factor;
       m[v].x = beta * m[v].x + g[v].x;
       m[v].y = beta * m[v].y + g[v].y;
       m[v].z = beta * m[v].z + g[v].z;
@@ -80,6 +89,7 @@ __global__ __launch_bounds__(EW_THREADS) void momentum_kernel(const MatDesc* __r
       for (int v = 0; v < 4 * V; ++v) {
         const int64_t e = b0 + v * EW_THREADS + threadIdx.x;
         if (e < end) {
+          if (CLIP) g[v] *= clip.factor;
           const float mn = beta * m[v] + g[v];
           M[e] = mn;
           const float u = nesterov(g[v], mn, beta);
@@ -103,9 +113,12 @@ __global__ __launch_bounds__(EW_THREADS) void norm_finalize_kernel(const MatDesc
 }
 
 hipError_t launch_momentum(const MatDesc* d, const EwItem* items, int n_items, const int32_t* fin, int n_fin,
-                           float beta, hipStream_t s) {
+                           float beta, const float* record, hipStream_t s) {
   if (n_items == 0) return hipSuccess;
-  momentum_kernel<<<n_items, EW_THREADS, 0, s>>>(d, items, beta);
+  if (record)
+    momentum_kernel<true><<<n_items, EW_THREADS, 0, s>>>(d, items, beta, record);
+  else
+    momentum_kernel<false><<<n_items, EW_THREADS, 0, s>>>(d, items, beta, nullptr);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || n_fin == 0) return e;
   norm_finalize_kernel<<<n_fin, EW_THREADS, 0, s>>>(d, fin);

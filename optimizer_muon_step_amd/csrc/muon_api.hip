@@ -16,6 +16,7 @@
 
 #include "../../include/muon.h"
 #include "api_internal.h"
+#include "grad_host.h"
 #include "muon_internal.h"
 #include "plan_host.h"
 
@@ -157,29 +158,6 @@ int g_time_kind = -1;
 std::vector<hipEvent_t> g_ev;  // start, end pairs
 size_t g_ev_used = 0;
 
-// Launch wrapper: brackets the launch with events when its family is timed.
-template <typename F>
-int timed(int kind, hipStream_t stream, F&& launch, const char* what) {
-  const bool on = (g_time_kind == kind);
-  hipError_t e;
-  if (on) {
-    if (g_ev_used + 2 > g_ev.size()) {
-      for (int k = 0; k < 2; ++k) {
-        hipEvent_t ev;
-        if ((e = hipEventCreate(&ev)) != hipSuccess) return fail_hip(e, "hipEventCreate");
-        g_ev.push_back(ev);
-      }
-    }
-    if ((e = hipEventRecord(g_ev[g_ev_used], stream)) != hipSuccess) return fail_hip(e, "hipEventRecord");
-  }
-  if ((e = launch()) != hipSuccess) return fail_hip(e, what);
-  if (on) {
-    if ((e = hipEventRecord(g_ev[g_ev_used + 1], stream)) != hipSuccess) return fail_hip(e, "hipEventRecord");
-    g_ev_used += 2;
-  }
-  return MUON_OK;
-}
-
 int capture_status(hipStream_t stream, bool* capturing) {
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   const hipError_t e = hipStreamIsCapturing(stream, &cs);
@@ -215,16 +193,16 @@ Tables tables_at(char* block, const PlanTables& t, int lane, char* ws) {
 // The kernel sequence of one lane: momentum and norm, cast, ns_steps
 // iterations of Gram, poly and update, apply.
 int launch_sequence(int mode, const Tables& v, float lr, float beta, int ns_steps, const float* coeffs, int stride,
-                    hipStream_t stream) {
+                    const float* record, hipStream_t stream) {
   const LaneTables& t = *v.t;
   int rc;
   if (mode == MODE_STEP) {
     rc = timed(MUON_KERNEL_MOMENTUM, stream,
-               [&] { return launch_momentum(v.desc, v.mom, t.n_mom, v.fin, t.n_fin, beta, stream); },
+               [&] { return launch_momentum(v.desc, v.mom, t.n_mom, v.fin, t.n_fin, beta, record, stream); },
                "momentum kernel launch");
     if (rc) return rc;
   }
-  rc = timed(MUON_KERNEL_CAST, stream, [&] { return launch_cast(v.desc, v.cast, t.n_cast, beta, mode == MODE_NS, stream); },
+  rc = timed(MUON_KERNEL_CAST, stream, [&] { return launch_cast(v.desc, v.cast, t.n_cast, beta, mode == MODE_NS, record, stream); },
              "cast kernel launch");
   if (rc) return rc;
   for (int k = 0; k < ns_steps; ++k) {
@@ -256,7 +234,7 @@ int launch_sequence(int mode, const Tables& v, float lr, float beta, int ns_step
     if (rc) return rc;
   }
   return timed(MUON_KERNEL_APPLY, stream,
-               [&] { return launch_apply(v.desc, v.apply, t.n_apply, lr, ns_steps & 1, mode == MODE_STEP, stream); },
+               [&] { return launch_apply(v.desc, v.apply, t.n_apply, lr, ns_steps & 1, mode == MODE_STEP, record, stream); },
                "apply kernel launch");
 }
 
@@ -276,7 +254,7 @@ namespace {
 
 int run(int mode, float* const* params, const float* const* grads, float* const* moms, uint16_t* const* upd,
         const uint16_t* const* xin, const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps,
-        const float* coeffs, int stride, hipStream_t stream) {
+        const float* coeffs, int stride, const float* record, hipStream_t stream) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
@@ -295,7 +273,7 @@ int run(int mode, float* const* params, const float* const* grads, float* const*
   if (L == 1 || capturing) {
     // one lane, or under capture: every lane in turn on the caller's stream
     for (int l = 0; l < L; ++l)
-      if ((rc = launch_sequence(mode, tables_at(block, p->t, l, p->ws), lr, beta, ns_steps, coeffs, stride, stream)))
+      if ((rc = launch_sequence(mode, tables_at(block, p->t, l, p->ws), lr, beta, ns_steps, coeffs, stride, record, stream)))
         return rc;
     return MUON_OK;
   }
@@ -307,7 +285,7 @@ int run(int mode, float* const* params, const float* const* grads, float* const*
   if ((e = hipEventRecord(ls.fork, stream)) != hipSuccess) return fail_hip(e, "hipEventRecord(fork)");
   for (int l = 0; l < L; ++l) {
     if ((e = hipStreamWaitEvent(ls.s[l], ls.fork, 0)) != hipSuccess) return fail_hip(e, "hipStreamWaitEvent(fork)");
-    if ((rc = launch_sequence(mode, tables_at(block, p->t, l, p->ws), lr, beta, ns_steps, coeffs, stride, ls.s[l])))
+    if ((rc = launch_sequence(mode, tables_at(block, p->t, l, p->ws), lr, beta, ns_steps, coeffs, stride, record, ls.s[l])))
       return rc;
     if ((e = hipEventRecord(ls.join[l], ls.s[l])) != hipSuccess) return fail_hip(e, "hipEventRecord(join)");
   }
@@ -318,12 +296,13 @@ int run(int mode, float* const* params, const float* const* grads, float* const*
 
 int step_entry(float* const* params, const float* const* grads, float* const* momentum, const muon_shape_t* shapes,
                int n, float lr, float beta, int ns_steps, const float* coeffs, int stride, uint16_t* const* updates,
-               hipStream_t stream) {
+               const float* record, hipStream_t stream) {
   clear_error();
   int rc = validate_step(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, stride, updates);
   if (rc || n == 0) return rc;
+  if (record && (rc = validate_step_record(params, momentum, updates, shapes, n, record))) return rc;
   return run(MODE_STEP, params, grads, momentum, updates, nullptr, shapes, n, lr, beta, ns_steps, coeffs, stride,
-             stream);
+             record, stream);
 }
 
 int ns_entry(const uint16_t* const* x, uint16_t* const* out, const muon_shape_t* shapes, int n, int ns_steps,
@@ -331,7 +310,8 @@ int ns_entry(const uint16_t* const* x, uint16_t* const* out, const muon_shape_t*
   clear_error();
   int rc = validate_ns(x, out, shapes, n, ns_steps, coeffs, stride);
   if (rc || n == 0) return rc;
-  return run(MODE_NS, nullptr, nullptr, nullptr, out, x, shapes, n, 0.0f, 0.0f, ns_steps, coeffs, stride, stream);
+  return run(MODE_NS, nullptr, nullptr, nullptr, out, x, shapes, n, 0.0f, 0.0f, ns_steps, coeffs, stride, nullptr,
+             stream);
 }
 
 // ---------------------------------------------------------------- AdamW ----
@@ -525,19 +505,30 @@ int muon_adamw_step(float* const* params, const float* const* grads, float* cons
 int muon_step_ex(float* const* params, const float* const* grads, float* const* momentum,
                  const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps, const float* coeffs,
                  uint16_t* const* updates, hipStream_t stream) {
-  return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 0, updates, stream);
+  return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 0, updates, nullptr,
+                    stream);
 }
 
 int muon_step(float* const* params, const float* const* grads, float* const* momentum,
               const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps, const float* coeffs,
               hipStream_t stream) {
-  return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 0, nullptr, stream);
+  return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 0, nullptr, nullptr,
+                    stream);
 }
 
 int muon_step_sched(float* const* params, const float* const* grads, float* const* momentum,
                     const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps, const float* coeffs,
                     uint16_t* const* updates, hipStream_t stream) {
-  return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 3, updates, stream);
+  return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 3, updates, nullptr,
+                    stream);
+}
+
+int muon_step_clip(float* const* params, const float* const* grads, float* const* momentum,
+                   const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps, const float* coeffs,
+                   uint16_t* const* updates, const float* record, hipStream_t stream) {
+  return c_entry([&] {
+    return step_entry(params, grads, momentum, shapes, n, lr, beta, ns_steps, coeffs, 3, updates, record, stream);
+  });
 }
 
 int muon_newton_schulz(const uint16_t* const* x, uint16_t* const* out, const muon_shape_t* shapes, int n,
@@ -612,7 +603,7 @@ int muon_set_lanes(int lanes) {
 
 int muon_timing_enable(int kernel) {
   clear_error();
-  if (kernel < -1 || kernel > MUON_KERNEL_ADAMW) return fail(MUON_EINVAL, "unknown kernel family %d", kernel);
+  if (kernel < -1 || kernel > MUON_KERNEL_GRAD_CLIP) return fail(MUON_EINVAL, "unknown kernel family %d", kernel);
   std::lock_guard<std::mutex> lock(api_mutex());
   g_time_kind = kernel;
   g_ev_used = 0;

@@ -4,17 +4,19 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "grad_types.h"
 #include "plan_types.h"
 
 namespace muon {
 
 // ---- host launchers (kernels_*.hip) ----
+// record: the {norm, factor} a step takes its gradients by, or null.
 hipError_t launch_momentum(const MatDesc* d, const EwItem* items, int n_items, const int32_t* fin, int n_fin,
-                           float beta, hipStream_t s);
+                           float beta, const float* record, hipStream_t s);
 hipError_t launch_cast(const MatDesc* d, const EwItem* items, int n_items, float beta, int from_bf16,
-                       hipStream_t s);
+                       const float* record, hipStream_t s);
 hipError_t launch_apply(const MatDesc* d, const EwItem* items, int n_items, float lr, int src,
-                        int write_w, hipStream_t s);
+                        int write_w, const float* record, hipStream_t s);
 // tile: the TileKind of the launch (large, small or medium tiles).
 hipError_t launch_gemm(int kind, const MatDesc* d, const GemmItem* items, int n_items, int src,
                        float ca, float cb, float cc, float* part, int tile, hipStream_t s);
@@ -32,6 +34,11 @@ hipError_t launch_gram_reduce(const MatDesc* d, const RedItem* items, int n_item
 hipError_t launch_ptr_patch(MatDesc* descs, const PtrPatch& p, hipStream_t s);
 hipError_t launch_blob_write(void* dst, const BlobChunk& c, hipStream_t s);
 hipError_t launch_adamw(const AdamDesc* d, const EwItem* items, int n_items, const AdamConst& c, hipStream_t s);
+
+// Gradient norm, clipping, and AdamW on clipped gradients: one launch each.
+hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t s);
+hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s);
 
 // Source and destination of the three arrays (param, exp_avg, exp_avg_sq)
 // of a delayed-untying copy.

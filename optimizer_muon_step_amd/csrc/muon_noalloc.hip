@@ -116,7 +116,7 @@ int noalloc_entry(float* const* params, const float* const* grads, float* const*
   // after a capture the device holds whatever the last replay wrote
   sc.known = !capturing;
   return launch_sequence(MODE_STEP, tables_at(base + sc.table_off, sc.tables, 0, base), lr, beta, ns_steps, coeffs, 0,
-                         stream);
+                         nullptr, stream);
 }
 
 }  // namespace

@@ -267,17 +267,22 @@ int validate_ns(const uint16_t* const* x, uint16_t* const* out, const muon_shape
   return check_ranges(r);
 }
 
+int check_adamw_scalars(float lr, float beta1, float beta2, float eps, int64_t step) {
+  if (!std::isfinite(lr)) return fail(MUON_EINVAL, "lr is not finite");
+  if (!std::isfinite(beta1) || beta1 < 0.0f || beta1 >= 1.0f) return fail(MUON_EINVAL, "beta1 = %g outside [0, 1)", (double)beta1);
+  if (!std::isfinite(beta2) || beta2 < 0.0f || beta2 >= 1.0f) return fail(MUON_EINVAL, "beta2 = %g outside [0, 1)", (double)beta2);
+  if (!std::isfinite(eps) || eps < 0.0f) return fail(MUON_EINVAL, "eps = %g is not finite and >= 0", (double)eps);
+  if (step < 1) return fail(MUON_EINVAL, "step = %lld: the first step is 1", (long long)step);
+  return MUON_OK;
+}
+
 int validate_adamw(float* const* params, const float* const* grads, float* const* u, float* const* v,
                    const int64_t* numels, const float* wd, int n, float lr, float beta1, float beta2, float eps,
                    int64_t step) {
   if (n < 0 || n > MUON_ADAMW_MAX_TENSORS) return fail(MUON_EINVAL, "n = %d outside [0, %d]", n, MUON_ADAMW_MAX_TENSORS);
   if (n > 0 && (!params || !grads || !u || !v || !numels))
     return fail(MUON_EINVAL, "params, grads, exp_avg, exp_avg_sq and numels arrays must not be NULL");
-  if (!std::isfinite(lr)) return fail(MUON_EINVAL, "lr is not finite");
-  if (!std::isfinite(beta1) || beta1 < 0.0f || beta1 >= 1.0f) return fail(MUON_EINVAL, "beta1 = %g outside [0, 1)", (double)beta1);
-  if (!std::isfinite(beta2) || beta2 < 0.0f || beta2 >= 1.0f) return fail(MUON_EINVAL, "beta2 = %g outside [0, 1)", (double)beta2);
-  if (!std::isfinite(eps) || eps < 0.0f) return fail(MUON_EINVAL, "eps = %g is not finite and >= 0", (double)eps);
-  if (step < 1) return fail(MUON_EINVAL, "step = %lld: the first step is 1", (long long)step);
+  if (const int rc = check_adamw_scalars(lr, beta1, beta2, eps, step)) return rc;
   std::vector<Range> r;
   r.reserve(4 * (size_t)n);
   for (int i = 0; i < n; ++i) {

@@ -43,6 +43,7 @@ int validate_step(float* const* params, const float* const* grads, float* const*
                   int n, float lr, float beta, int ns_steps, const float* coeffs, int stride, uint16_t* const* upd);
 int validate_ns(const uint16_t* const* x, uint16_t* const* out, const muon_shape_t* shapes, int n, int ns_steps,
                 const float* coeffs, int stride);
+int check_adamw_scalars(float lr, float beta1, float beta2, float eps, int64_t step);
 int validate_adamw(float* const* params, const float* const* grads, float* const* u, float* const* v,
                    const int64_t* numels, const float* wd, int n, float lr, float beta1, float beta2, float eps,
                    int64_t step);

@@ -1,0 +1,118 @@
+"""CPU checks of the gradient norm, clipping and clipped steps: the host code
+under sanitizers, refusals at the C entries and in the binding, and the oracle
+against closed forms."""
+import math
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+from optimizer_muon_step_amd import _lib
+from oracle import grad_oracle as go
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "optimizer_muon_step_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from optimizer_muon_step_amd import build
+        build.build()
+    return _lib.load()
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no host C++ compiler")
+def test_host_code_under_address_and_ub_sanitizers(tmp_path):
+    exe = tmp_path / "grad_check"
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
+           "-fno-sanitize-recover=undefined", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__",
+           "-I", "/opt/rocm/include", "-I", CSRC, os.path.join(CSRC, "grad_host.cpp"),
+           os.path.join(CSRC, "plan_host.cpp"), os.path.join(ROOT, "tests", "native", "grad_check.cpp"),
+           "-o", str(exe)]
+    build = subprocess.run(cmd, capture_output=True, text=True)
+    assert build.returncode == 0, build.stdout + build.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip() == "ok", run.stdout + run.stderr
+
+
+def test_entries_refuse_before_any_hip_call(lib):
+    """Addresses that no GPU has: a refusal must come before they are used."""
+    g, o = _lib.ptr_array([0x100000]), _lib.ptr_array([0x200000])
+    n1 = _lib.int64_array([64])
+    import ctypes
+    t32 = (ctypes.c_int * 1)(0)
+    bad = (ctypes.c_int * 1)(7)
+    rec, ws = 0x900000, 0xa00000
+    text = lambda: lib.muon_last_error().decode()  # noqa: E731
+    assert lib.muon_grad_norm(g, n1, bad, 1, 1.0, 1.0, rec, ws, None) == -1 and "dtypes[0] = 7" in text()
+    assert lib.muon_grad_norm(g, n1, t32, 1, -1.0, 1.0, rec, ws, None) == -1 and "max_norm" in text()
+    assert lib.muon_grad_norm(g, n1, t32, 1, 1.0, math.nan, rec, ws, None) == -1 and "scale" in text()
+    assert lib.muon_grad_norm(g, n1, t32, 1, 1.0, 1.0, None, ws, None) == -1 and "record" in text()
+    assert lib.muon_grad_norm(g, n1, t32, 1, 1.0, 1.0, rec, None, None) == -1 and "workspace" in text()
+    assert lib.muon_grad_clip(g, o, n1, t32, bad, 1, 1.0, 1.0, rec, ws, None) == -1 and "out_dtypes" in text()
+    assert lib.muon_grad_clip(g, _lib.ptr_array([0x100010]), n1, t32, t32, 1, 1.0, 1.0, rec, ws, None) == -1
+    assert "overlaps" in text()
+    P = [_lib.ptr_array([0x10000 * (k + 1)]) for k in range(4)]
+    adamw = lambda **kw: lib.muon_adamw_step_clip(  # noqa: E731
+        P[0], P[1], kw.get("t", t32), P[2], P[3], n1, None, 1, kw.get("lr", 1e-3), 0.9, 0.999, 1e-8,
+        kw.get("step", 1), kw.get("rec", rec), None)
+    assert adamw(step=0) == -1 and "step" in text()
+    assert adamw(lr=math.inf) == -1 and "lr" in text()
+    assert adamw(t=bad) == -1 and "grad_dtypes" in text()
+    assert adamw(rec=0x10004) == -1 and "overlaps" in text()
+    shapes = _lib.shape_array([(4, 4)])
+    c = _lib.float_array([1.0, 0.0, 0.0])
+    assert lib.muon_step_clip(P[0], P[1], P[2], shapes, 1, 0.02, 0.95, 1, c, None, 0x900001, None) == -1
+    assert "record" in text()
+    assert lib.muon_step_clip(P[0], P[1], P[2], shapes, 1, 0.02, 0.95, 1, c, None, 0x30000, None) == -1
+    assert "overlaps" in text()
+    # nothing to do: no device needed
+    assert lib.muon_adamw_step_clip(None, None, None, None, None, None, None, 0, 1e-3, 0.9, 0.999, 1e-8, 1, rec,
+                                    None) == 0
+    assert lib.muon_step_clip(P[0], P[1], P[2], shapes, 0, 0.02, 0.95, 1, c, None, rec, None) == 0
+
+
+def test_binding_refuses():
+    import torch
+
+    import optimizer_muon_step_amd as mu
+    cpu = torch.zeros(4)
+    for call in (lambda: mu.muon_grad_norm([cpu]), lambda: mu.muon_grad_clip([cpu], 1.0),
+                 lambda: mu.muon_adamw_step([cpu], [cpu.bfloat16()], [cpu], [cpu], 1e-3)):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
+    with pytest.raises(ValueError, match="expected a tensor"):
+        mu.muon_grad_norm([None])
+    with pytest.raises(ValueError, match="not torch.float64"):
+        mu.muon_grad_norm([cpu.double()])
+    with pytest.raises(ValueError, match="not torch.int32"):
+        mu.muon_grad_clip([cpu.int()], 1.0)
+    with pytest.raises(ValueError, match="expected float32"):
+        mu.muon_adamw_step([cpu.bfloat16()], [cpu.bfloat16()], [cpu], [cpu], 1e-3)
+
+
+def test_dense_layouts():
+    import torch
+
+    import optimizer_muon_step_amd as mu
+    t = torch.zeros(4, 5, 6)
+    assert mu._dense(t) and mu._dense(t.permute(2, 0, 1)) and mu._dense(t[:, :1].permute(1, 2, 0)) is False
+    assert mu._dense(torch.zeros(1, 5).t()) and mu._dense(torch.zeros(3, 1, 7).permute(2, 1, 0))
+    assert not mu._dense(torch.zeros(4, 5)[:, :3]) and not mu._dense(torch.zeros(1).expand(4))
+    assert not mu._dense(torch.zeros(8)[::2])
+
+
+def test_oracle_closed_forms():
+    norm, factor = go.norm_factor([np.array([3.0]), np.array([0.0, 4.0])], 1.0)
+    assert norm == 5.0 and factor == 1.0 / (5.0 + 1e-6)
+    assert go.norm_factor([np.array([3.0, 4.0])], 10.0, 0.5) == (2.5, 0.5)
+    assert go.norm_factor([], 0.0) == (0.0, 0.0) and go.norm_factor([]) == (0.0, 1.0)
+    assert go.norm_factor([np.array([math.inf])], 1.0) == (math.inf, 0.0)
+    n, f = go.norm_factor([np.array([math.nan])])
+    assert math.isnan(n) and math.isnan(f)
+    # halves and ties of the 16-bit roundings
+    assert go.rounded(np.float32(1 + 2.0 ** -8), "bf16") == 1.0 and go.rounded(np.float32(1 + 3 * 2.0 ** -8), "bf16") == 1 + 2.0 ** -6
+    assert go.rounded(np.float32(70000), "fp16") == np.inf and go.rounded(np.float32(2.0 ** -25), "fp16") == 0.0
