@@ -10,7 +10,6 @@ and return without synchronising.
 from __future__ import annotations
 
 import ctypes
-from array import array
 
 from . import _lib
 
@@ -220,49 +219,17 @@ def _any_16_bit(ts):
     return any(getattr(t, "dtype", None) in halves for t in ts)
 
 
-def _dense(t):
-    """Whether t's elements fill one stretch of memory, each once, in any order of dimensions."""
-    want = 1
-    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
-        if stride != want:
-            return False
-        want *= size
-    return True
-
-
-_TYPE_CODES = {}
+def _as_list(ts):
+    return ts if isinstance(ts, (list, tuple)) else list(ts)
 
 
 def _flat_list(ts, what, any_type, dense):
     """(addresses, element counts, type codes) of a list of tensors taken flat, as C arrays."""
     import torch
-    if not _TYPE_CODES:
-        _TYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    dev = None
-    ptrs, numels, types = array("Q"), array("q"), array("i")
-    for i, t in enumerate(ts):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{what}[{i}]: expected a tensor")
-        code = _TYPE_CODES.get(t.dtype, -1)
-        if code < 0 or (code > 0 and not any_type):
-            raise ValueError(f"{what}[{i}]: expected {'float32, bfloat16 or float16' if any_type else 'float32'}, "
-                             f"not {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{what}[{i}]: expected a tensor on the GPU")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{what}[{i}] is on GPU {t.get_device()}, the current one is {dev}")
-        if not (t.is_contiguous() or (dense and _dense(t))):
-            raise ValueError(f"{what}[{i}]: expected a {'dense' if dense else 'contiguous'} tensor")
-        ptrs.append(t.data_ptr())
-        numels.append(t.numel())
-        types.append(code)
+    ptrs, numels, types, dev = _lib.load_tensor_args().flat(ts, what, any_type, dense)
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors on GPU {dev}, the current one is {torch.cuda.current_device()}")
     return ptrs, numels, types
-
-
-def _address(a):
-    return a.buffer_info()[0]
 
 
 def _record_ptr(record):
@@ -355,15 +322,16 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
 
 
 def _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip):
+    n = len(params)
     lists = [_flat_list(ts, what, any_type=what == "grads", dense=False)
              for ts, what in ((params, "params"), (grads, "grads"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"))]
     (p, numels, _), (g, g_numels, types), (u, u_numels, _), (v, v_numels, _) = lists
     if not numels == g_numels == u_numels == v_numels:
-        i = next(i for i in range(len(numels)) if len({a[i] for a in (numels, g_numels, u_numels, v_numels)}) != 1)
+        i = next(i for i in range(n) if len({ts[i].numel() for ts in (params, grads, exp_avg, exp_avg_sq)}) != 1)
         raise ValueError(f"tensor {i}: element counts differ")
     record = None if clip is None else _record_ptr(clip)
-    _check(_lib.load().muon_adamw_step_clip(_address(p), _address(g), _address(types), _address(u), _address(v),
-                                            _address(numels), _lib.float_array(wds), len(p), float(lr),
+    _check(_lib.load().muon_adamw_step_clip(p, g, types, u, v,
+                                            numels, _lib.float_array(wds), n, float(lr),
                                             float(betas[0]), float(betas[1]), float(eps), int(step), record,
                                             _stream_handle(stream)))
 
@@ -378,11 +346,12 @@ def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=
     as `clip` to muon_step and muon_adamw_step, which then take the gradients
     clipped without a pass that writes them back.  `record` is a tensor of 2
     to fill instead of a new one."""
+    grads = _as_list(grads)
     ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
     lib = _lib.load()
     with _on_stream(stream):
         record, ws, st = _norm_buffers(record)
-        _check(lib.muon_grad_norm(_address(ptrs), _address(numels), _address(types), len(ptrs), float(max_norm),
+        _check(lib.muon_grad_norm(ptrs, numels, types, len(grads), float(max_norm),
                                   float(scale), record.data_ptr(), ws.data_ptr(), st))
     return record
 
@@ -393,21 +362,23 @@ def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=No
     same shapes and memory order and of any of the three types (16-bit
     gradients into float32 ones, say).  Returns the record {norm, factor};
     the norm is the one before clipping."""
+    grads = _as_list(grads)
     ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
     if outs is None:
         out_ptrs, out_types = ptrs, types
     else:
-        if len(outs) != len(ptrs):
+        outs = _as_list(outs)
+        if len(outs) != len(grads):
             raise ValueError("grads and outs must have the same length")
         out_ptrs, _, out_types = _flat_list(outs, "outs", any_type=True, dense=True)
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            if g.shape != o.shape or (g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous())):
-                raise ValueError(f"outs[{i}]: shape or memory order differs from grads[{i}]")
+        i = _lib.load_tensor_args().first_unlike(grads, outs)
+        if i >= 0:
+            raise ValueError(f"outs[{i}]: shape or memory order differs from grads[{i}]")
     lib = _lib.load()
     with _on_stream(stream):
         record, ws, st = _norm_buffers(record)
-        _check(lib.muon_grad_clip(_address(ptrs), _address(out_ptrs), _address(numels), _address(types),
-                                  _address(out_types), len(ptrs), float(max_norm), float(scale), record.data_ptr(),
+        _check(lib.muon_grad_clip(ptrs, out_ptrs, numels, types,
+                                  out_types, len(grads), float(max_norm), float(scale), record.data_ptr(),
                                   ws.data_ptr(), st))
     return record
 

@@ -51,6 +51,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_tensor_args = None
 
 
 def load() -> ctypes.CDLL:
@@ -68,6 +69,21 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+def load_tensor_args():
+    """The compiled reader of tensor lists; raises if it has not been built."""
+    global _tensor_args
+    if _tensor_args is None:
+        import torch  # noqa: F401  (its libraries, which the module links against)
+        try:
+            from . import _tensor_args as module
+        except ImportError as e:
+            raise RuntimeError(
+                "_tensor_args.so is missing: build it with `python -m optimizer_muon_step_amd.build` "
+                f"(or __graft_entry__.build()); there is no fallback implementation ({e})") from e
+        _tensor_args = module
+    return _tensor_args
 
 
 def ptr_array(ptrs):

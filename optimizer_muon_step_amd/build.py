@@ -1,5 +1,6 @@
 """Build libmuon.so (the gfx950 HIP kernels and the C ABI) in place with
-hipcc, and the plain C caller muon_c_example linked against it."""
+hipcc, the plain C caller muon_c_example linked against it, and the binding's
+reader of tensor lists."""
 from __future__ import annotations
 
 import hashlib
@@ -7,12 +8,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmuon.so")
+TENSOR_ARGS = os.path.join(HERE, "_tensor_args.so")
 C_EXAMPLE = os.path.join(HERE, "muon_c_example")
 SOURCES = ["muon_api.hip", "muon_noalloc.hip", "plan_host.cpp", "kernels_tables.hip", "kernels_momentum.hip", "kernels_elementwise.hip",
            "kernels_ns.hip", "kernels_ns_gram.hip", "kernels_ns_fused.hip", "kernels_adamw.hip", "grad_api.hip",
@@ -108,7 +111,31 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB,
     os.replace(tmp, out)
     if out == LIB:
         build_c_example(verbose)
+        build_tensor_args(verbose)
     return out
+
+
+def build_tensor_args(verbose: bool = False) -> str:
+    """Compile csrc/tensor_args.cpp with the host C++ compiler against torch."""
+    import torch
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no host C++ compiler")
+    at = os.path.dirname(torch.__file__)
+    tmp = TENSOR_ARGS + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(at, "include"), "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_args.cpp"),
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"{cxx} failed with exit code {res.returncode}")
+    os.replace(tmp, TENSOR_ARGS)
+    return TENSOR_ARGS
 
 
 def build_c_example(verbose: bool = False) -> str:

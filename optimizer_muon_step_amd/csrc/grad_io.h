@@ -13,10 +13,12 @@ namespace grad {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Vectors that promise only their element's alignment: tensors may start
-// anywhere in a flat buffer, and gfx950 loads and stores such vectors whole.
+// vec: four elements; wide: sixteen bytes, for passes that only read.  Both
+// promise only their element's alignment: tensors may start anywhere in a flat
+// buffer, and gfx950 loads and stores such vectors whole.
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint16_t u16x8_u __attribute__((ext_vector_type(8), aligned(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
@@ -27,6 +29,7 @@ template <>
 struct Elem<GRAD_FP32> {
   typedef float scalar;
   typedef f32x4_u vec;
+  typedef f32x4_u wide;
   static __device__ __forceinline__ f32x4 widen(vec w) { return f32x4{w.x, w.y, w.z, w.w}; }
   static __device__ __forceinline__ float widen1(scalar w) { return w; }
   static __device__ __forceinline__ vec narrow(f32x4 v) { return vec{v.x, v.y, v.z, v.w}; }
@@ -38,6 +41,7 @@ template <>
 struct Elem<GRAD_BF16> {
   typedef uint16_t scalar;
   typedef u16x4_u vec;
+  typedef u16x8_u wide;
   static __device__ __forceinline__ f32x4 widen(vec w) {
     return f32x4{bf16_bits_to_f32(w.x), bf16_bits_to_f32(w.y), bf16_bits_to_f32(w.z), bf16_bits_to_f32(w.w)};
   }
@@ -53,6 +57,7 @@ template <>
 struct Elem<GRAD_FP16> {
   typedef uint16_t scalar;
   typedef u16x4_u vec;
+  typedef u16x8_u wide;
   static __device__ __forceinline__ f32x4 widen(vec w) {
     return __builtin_convertvector(__builtin_bit_cast(f16x4, u16x4{w.x, w.y, w.z, w.w}), f32x4);
   }

@@ -29,14 +29,21 @@ constexpr int64_t GRAD_MAX_NUMEL = (int64_t)1 << 35;
 
 // ---- global norm ----
 constexpr int NORM_CHUNK_BYTES = 16384;  // 4 x 16 bytes per thread
-constexpr int NORM_MAX_BLOCKS = 2048;    // partial sums in the workspace
+constexpr int NORM_MAX_BLOCKS = 1024;    // partial sums in the workspace
+constexpr int NORM_GROUP = 32;           // blocks that count on one counter
+constexpr int NORM_MAX_GROUPS = NORM_MAX_BLOCKS / NORM_GROUP;
 constexpr int norm_chunk(int type) { return NORM_CHUNK_BYTES / grad_type_bytes(type); }
 
-// The caller's workspace: `arrived` counts the blocks of a call that have
-// stored their partial sum, and is zero between calls.
-struct NormWorkspace {
+// The caller's workspace.  `arrived` counts the blocks of a group that have
+// stored their partial sum, `groups` the groups that are complete; both are
+// zero between calls.  Each counter has a 128-byte line of its own.
+struct NormCounter {
   uint32_t arrived;
-  uint32_t pad_[15];
+  uint32_t pad_[31];
+};
+struct NormWorkspace {
+  NormCounter groups;
+  NormCounter group[NORM_MAX_GROUPS];
   double part[NORM_MAX_BLOCKS];
 };
 

@@ -105,8 +105,10 @@ __global__ __launch_bounds__(EW_THREADS) void adamw_kernel(const AdamDesc* __res
 namespace {
 
 // One chunk of len elements on gradients of type TG: g' = fp32(g) * factor,
-// one rounding, then adamw_elem.
-template <int TG>
+// one rounding, then adamw_elem.  All loads go out before any arithmetic; a
+// partial chunk's vectors that fit move whole, the up to 3 elements behind
+// them one per thread.
+template <int TG, bool FULL>
 __device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, int64_t off, int len, float factor,
                                                  float decay) {
   typedef grad::Elem<TG> E;
@@ -116,44 +118,49 @@ __device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, i
   const MUON_GLOBAL typename E::scalar* G = gptr(static_cast<const typename E::scalar*>(a.g[t])) + off;
   MUON_GLOBAL float* U = gptr(a.u[t]) + off;
   MUON_GLOBAL float* Q = gptr(a.v[t]) + off;
-  if (len == ADAMC_CHUNK) {
-    MUON_GLOBAL vec* p4 = reinterpret_cast<MUON_GLOBAL vec*>(P);
-    const MUON_GLOBAL typename E::vec* g4 = reinterpret_cast<const MUON_GLOBAL typename E::vec*>(G);
-    MUON_GLOBAL vec* u4 = reinterpret_cast<MUON_GLOBAL vec*>(U);
-    MUON_GLOBAL vec* v4 = reinterpret_cast<MUON_GLOBAL vec*>(Q);
-    vec p[V], u[V], v[V];
-    typename E::vec gw[V];
+  MUON_GLOBAL vec* p4 = reinterpret_cast<MUON_GLOBAL vec*>(P);
+  const MUON_GLOBAL typename E::vec* g4 = reinterpret_cast<const MUON_GLOBAL typename E::vec*>(G);
+  MUON_GLOBAL vec* u4 = reinterpret_cast<MUON_GLOBAL vec*>(U);
+  MUON_GLOBAL vec* v4 = reinterpret_cast<MUON_GLOBAL vec*>(Q);
+  const int n4 = len / 4;
+  auto has = [&](int k) { return FULL || k * GRAD_THREADS + (int)threadIdx.x < n4; };
+  vec p[V], u[V], v[V];
+  typename E::vec gw[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) gw[k] = __builtin_nontemporal_load(&g4[k * GRAD_THREADS + threadIdx.x]);
+  for (int k = 0; k < V; ++k)
+    if (has(k)) gw[k] = __builtin_nontemporal_load(&g4[k * GRAD_THREADS + threadIdx.x]);
 #pragma unroll
-    for (int k = 0; k < V; ++k) u[k] = __builtin_nontemporal_load(&u4[k * GRAD_THREADS + threadIdx.x]);
+  for (int k = 0; k < V; ++k)
+    if (has(k)) u[k] = __builtin_nontemporal_load(&u4[k * GRAD_THREADS + threadIdx.x]);
 #pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = __builtin_nontemporal_load(&v4[k * GRAD_THREADS + threadIdx.x]);
+  for (int k = 0; k < V; ++k)
+    if (has(k)) v[k] = __builtin_nontemporal_load(&v4[k * GRAD_THREADS + threadIdx.x]);
 #pragma unroll
-    for (int k = 0; k < V; ++k) p[k] = __builtin_nontemporal_load(&p4[k * GRAD_THREADS + threadIdx.x]);
+  for (int k = 0; k < V; ++k)
+    if (has(k)) p[k] = __builtin_nontemporal_load(&p4[k * GRAD_THREADS + threadIdx.x]);
+  if (!FULL && (int)threadIdx.x < len % 4) {
+    const int e = 4 * n4 + threadIdx.x;
+    float pe = P[e], ue = U[e], ve = Q[e];
+    adamw_elem(pe, E::widen1(G[e]) * factor, ue, ve, a, decay);
+    P[e] = pe;
+    U[e] = ue;
+    Q[e] = ve;
+  }
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const f32x4 g = E::widen(gw[k]) * factor;
+  for (int k = 0; k < V; ++k) {
+    if (!has(k)) continue;
+    const f32x4 g = E::widen(gw[k]) * factor;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float pe = p[k][e], ue = u[k][e], ve = v[k][e];
-        adamw_elem(pe, g[e], ue, ve, a, decay);
-        p[k][e] = pe;
-        u[k][e] = ue;
-        v[k][e] = ve;
-      }
-      __builtin_nontemporal_store(u[k], &u4[k * GRAD_THREADS + threadIdx.x]);
-      __builtin_nontemporal_store(v[k], &v4[k * GRAD_THREADS + threadIdx.x]);
-      __builtin_nontemporal_store(p[k], &p4[k * GRAD_THREADS + threadIdx.x]);
+    for (int e = 0; e < 4; ++e) {
+      float pe = p[k][e], ue = u[k][e], ve = v[k][e];
+      adamw_elem(pe, g[e], ue, ve, a, decay);
+      p[k][e] = pe;
+      u[k][e] = ue;
+      v[k][e] = ve;
     }
-  } else {
-    for (int e = threadIdx.x; e < len; e += GRAD_THREADS) {
-      float pe = P[e], ue = U[e], ve = Q[e];
-      adamw_elem(pe, E::widen1(G[e]) * factor, ue, ve, a, decay);
-      P[e] = pe;
-      U[e] = ue;
-      Q[e] = ve;
-    }
+    __builtin_nontemporal_store(u[k], &u4[k * GRAD_THREADS + threadIdx.x]);
+    __builtin_nontemporal_store(v[k], &v4[k * GRAD_THREADS + threadIdx.x]);
+    __builtin_nontemporal_store(p[k], &p4[k * GRAD_THREADS + threadIdx.x]);
   }
 }
 
@@ -173,7 +180,11 @@ __global__ __launch_bounds__(GRAD_THREADS) void adamw_clip_kernel(const AdamClip
   const int64_t off = (int64_t)(it - a.start[t]) * ADAMC_CHUNK;
   const int len = it + 1 == a.start[t + 1] ? (int)(tail >> 4) : ADAMC_CHUNK;
   const float decay = 1.0f - a.lr * a.wd[(tail >> 2) & 3];
-  grad::with_type(tail & 3, [&](auto tg) { adamw_clip_chunk<decltype(tg)::value>(a, t, off, len, factor, decay); });
+  grad::with_type(tail & 3, [&](auto tg) {
+    constexpr int TG = decltype(tg)::value;
+    if (len == ADAMC_CHUNK) adamw_clip_chunk<TG, true>(a, t, off, len, factor, decay);
+    else adamw_clip_chunk<TG, false>(a, t, off, len, factor, decay);
+  });
 }
 
 hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s) {

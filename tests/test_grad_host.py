@@ -86,9 +86,11 @@ def test_binding_refuses():
             call()
     with pytest.raises(ValueError, match="expected a tensor"):
         mu.muon_grad_norm([None])
-    with pytest.raises(ValueError, match="not torch.float64"):
+    with pytest.raises(TypeError, match="list of tensors"):
+        _lib.load_tensor_args().flat(3, "grads", True, True)
+    with pytest.raises(ValueError, match="bfloat16 or float16, not Double"):
         mu.muon_grad_norm([cpu.double()])
-    with pytest.raises(ValueError, match="not torch.int32"):
+    with pytest.raises(ValueError, match="not Int"):
         mu.muon_grad_clip([cpu.int()], 1.0)
     with pytest.raises(ValueError, match="expected float32"):
         mu.muon_adamw_step([cpu.bfloat16()], [cpu.bfloat16()], [cpu], [cpu], 1e-3)
@@ -99,10 +101,28 @@ def test_dense_layouts():
 
     import optimizer_muon_step_amd as mu
     t = torch.zeros(4, 5, 6)
-    assert mu._dense(t) and mu._dense(t.permute(2, 0, 1)) and mu._dense(t[:, :1].permute(1, 2, 0)) is False
-    assert mu._dense(torch.zeros(1, 5).t()) and mu._dense(torch.zeros(3, 1, 7).permute(2, 1, 0))
-    assert not mu._dense(torch.zeros(4, 5)[:, :3]) and not mu._dense(torch.zeros(1).expand(4))
-    assert not mu._dense(torch.zeros(8)[::2])
+    for g in (t, t.permute(2, 0, 1), t[1:3], torch.zeros(1, 5).t(), torch.zeros(3, 1, 7).permute(2, 1, 0),
+              torch.zeros(0, 3).t(), torch.zeros(())):  # only the device is wrong
+        with pytest.raises(ValueError, match="on the GPU"):
+            mu.muon_grad_norm([t, g])
+    for g in (t[:, :1].permute(1, 2, 0), torch.zeros(4, 5)[:, :3], torch.zeros(1).expand(4), torch.zeros(8)[::2],
+              t.to_sparse(), torch._neg_view(t)):
+        with pytest.raises(ValueError, match=r"grads\[0\]: expected a dense tensor"):
+            mu.muon_grad_norm([g])
+    with pytest.raises(ValueError, match=r"params\[0\]: expected a contiguous tensor"):
+        mu.muon_adamw_step([t.permute(2, 0, 1)], [t.half()], [t], [t], 1e-3)
+
+
+def test_lists_alike():
+    import torch
+
+    from optimizer_muon_step_amd import _lib as lib
+    unlike = lib.load_tensor_args().first_unlike
+    t = torch.zeros(4, 5)
+    assert unlike([t, t], (t, t.clone())) == -1 and unlike([], []) == -1
+    assert unlike([t, t], [t, t.t()]) == 1 and unlike([t.t()], [t.t().clone()]) == -1
+    assert unlike([t], [t.view(5, 4)]) == 0 and unlike([t], [None]) == 0
+    assert unlike([torch.zeros(1, 5)], [torch.zeros(5, 1).t()]) == -1
 
 
 def test_oracle_closed_forms():
