@@ -44,7 +44,8 @@ int muon_grad_norm(const void* const* grads, const int64_t* numels, const int* d
     clear_error();
     const int rc = validate_grad_norm(grads, numels, dtypes, n, max_norm, scale, record, workspace);
     if (rc) return rc;
-    std::vector<NormArgs> norm = norm_launches(grads, numels, dtypes, n);
+    // without a limit the norm is wanted for itself
+    std::vector<NormArgs> norm = norm_launches(grads, numels, dtypes, n, std::isinf(max_norm) ? 0 : NORM_KEEP_BYTES);
     std::lock_guard<std::mutex> lock(api_mutex());
     return enqueue_norm(norm, max_norm, scale, record, workspace, stream);
   });
@@ -57,8 +58,11 @@ int muon_grad_clip(const void* const* grads, void* const* outs, const int64_t* n
     clear_error();
     int rc = validate_grad_clip(grads, outs, numels, dtypes, out_dtypes, n, max_norm, scale, record, workspace);
     if (rc) return rc;
-    std::vector<NormArgs> norm = norm_launches(grads, numels, dtypes, n);
     std::vector<ClipArgs> clip = clip_launches(grads, outs, numels, dtypes, out_dtypes, n);
+    // in place the gradients are usually not read again
+    bool in_place = true;
+    for (const ClipArgs& a : clip) in_place = in_place && a.in_place;
+    std::vector<NormArgs> norm = norm_launches(grads, numels, dtypes, n, in_place ? 0 : NORM_KEEP_BYTES);
     std::lock_guard<std::mutex> lock(api_mutex());
     if ((rc = enqueue_norm(norm, max_norm, scale, record, workspace, stream))) return rc;
     for (ClipArgs& a : clip) {

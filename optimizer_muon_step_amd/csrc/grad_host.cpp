@@ -182,7 +182,8 @@ int validate_step_record(float* const* params, float* const* moms, uint16_t* con
   return check_spans(s);
 }
 
-std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* numels, const int* types, int n) {
+std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* numels, const int* types, int n,
+                                    int64_t keep_bytes) {
   std::vector<NormArgs> out(1, NormArgs{});
   for (int i = 0; i < n; ++i) {
     if (numels[i] == 0) continue;
@@ -199,6 +200,12 @@ std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* num
   }
   out.front().first = 1;
   out.back().last = 1;
+  int64_t left = keep_bytes;
+  for (auto a = out.rbegin(); a != out.rend(); ++a) {
+    const int64_t items = std::min<int64_t>(a->start[a->n], left / NORM_CHUNK_BYTES);
+    a->keep_from = a->start[a->n] - (int32_t)items;
+    left -= items * NORM_CHUNK_BYTES;
+  }
   int32_t most = 1;
   for (const NormArgs& a : out) most = std::max(most, a.start[a.n]);
   for (NormArgs& a : out) a.blocks = std::min(most, (int32_t)NORM_MAX_BLOCKS);
@@ -211,9 +218,12 @@ std::vector<ClipArgs> clip_launches(const void* const* grads, void* const* outs,
   for (int i = 0; i < n; ++i) {
     if (numels[i] == 0) continue;
     const Cut c = cut_of(numels[i], CLIP_CHUNK);
-    if (out.empty() || out.back().n == CLIP_TENSORS || out.back().items + c.items > MAX_LAUNCH_ITEMS)
+    if (out.empty() || out.back().n == CLIP_TENSORS || out.back().items + c.items > MAX_LAUNCH_ITEMS) {
       out.push_back(ClipArgs{});
+      out.back().in_place = 1;
+    }
     ClipArgs& a = out.back();
+    a.in_place &= grads[i] == outs[i];
     a.tail[a.n] = c.last << 4 | (uint32_t)out_types[i] << 2 | (uint32_t)types[i];
     a.in[a.n] = grads[i];
     a.out[a.n] = outs[i];
@@ -227,10 +237,13 @@ std::vector<AdamClipArgs> adamw_clip_launches(float* const* params, const void* 
                                               float* const* u, float* const* v, const int64_t* numels,
                                               const float* wd, int n) {
   std::vector<AdamClipArgs> out;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) total += numels[i];
+  const int chunk = total >= ADAMC_LONG_MIN ? ADAMC_LONG_CHUNK : ADAMC_CHUNK;
   int decays = 0;  // distinct ones of the last launch so far
   for (int i = 0; i < n; ++i) {
     if (numels[i] == 0) continue;
-    const Cut c = cut_of(numels[i], ADAMC_CHUNK);
+    const Cut c = cut_of(numels[i], chunk);
     const float lambda = wd ? wd[i] : 0.0f;
     int k = 0;
     if (!out.empty())
@@ -238,6 +251,7 @@ std::vector<AdamClipArgs> adamw_clip_launches(float* const* params, const void* 
     if (out.empty() || out.back().n == ADAMC_TENSORS || k == ADAMC_DECAYS ||
         out.back().items + c.items > MAX_LAUNCH_ITEMS) {
       out.push_back(AdamClipArgs{});
+      out.back().chunk = chunk;
       k = decays = 0;
     }
     AdamClipArgs& a = out.back();

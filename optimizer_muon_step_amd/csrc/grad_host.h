@@ -30,7 +30,9 @@ int validate_step_record(float* const* params, float* const* moms, uint16_t* con
 // ---- launch tables: pointers, items and flags; scalars are the caller's ----
 // Tensors without elements take no part.  There is always at least one norm
 // launch (it writes the record), all of one grid; the others may have none.
-std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* numels, const int* types, int n);
+// keep_bytes: how much of the list's end the norm reads so as to stay cached.
+std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* numels, const int* types, int n,
+                                    int64_t keep_bytes);
 std::vector<ClipArgs> clip_launches(const void* const* grads, void* const* outs, const int64_t* numels,
                                     const int* types, const int* out_types, int n);
 std::vector<AdamClipArgs> adamw_clip_launches(float* const* params, const void* const* grads, const int* types,

@@ -108,12 +108,12 @@ namespace {
 // one rounding, then adamw_elem.  All loads go out before any arithmetic; a
 // partial chunk's vectors that fit move whole, the up to 3 elements behind
 // them one per thread.
-template <int TG, bool FULL>
+template <int TG, int CHUNK, bool FULL>
 __device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, int64_t off, int len, float factor,
                                                  float decay) {
   typedef grad::Elem<TG> E;
   typedef grad::f32x4_u vec;
-  constexpr int V = ADAMC_CHUNK / (4 * GRAD_THREADS);
+  constexpr int V = CHUNK / (4 * GRAD_THREADS);
   MUON_GLOBAL float* P = gptr(a.p[t]) + off;
   const MUON_GLOBAL typename E::scalar* G = gptr(static_cast<const typename E::scalar*>(a.g[t])) + off;
   MUON_GLOBAL float* U = gptr(a.u[t]) + off;
@@ -168,6 +168,7 @@ __device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, i
 
 // The AdamW step on clipped gradients: the factor is read from the record on
 // the device.  A norm that is not finite leaves everything as it was.
+template <int CHUNK>
 __global__ __launch_bounds__(GRAD_THREADS) void adamw_clip_kernel(const AdamClipArgs a) {
   float factor = 1.0f;
   if (a.record) {
@@ -177,19 +178,22 @@ __global__ __launch_bounds__(GRAD_THREADS) void adamw_clip_kernel(const AdamClip
   const int it = blockIdx.x;
   const int t = grad::find_tensor(a.start, 0, a.n, it);
   const uint32_t tail = a.tail[t];
-  const int64_t off = (int64_t)(it - a.start[t]) * ADAMC_CHUNK;
-  const int len = it + 1 == a.start[t + 1] ? (int)(tail >> 4) : ADAMC_CHUNK;
+  const int64_t off = (int64_t)(it - a.start[t]) * CHUNK;
+  const int len = it + 1 == a.start[t + 1] ? (int)(tail >> 4) : CHUNK;
   const float decay = 1.0f - a.lr * a.wd[(tail >> 2) & 3];
   grad::with_type(tail & 3, [&](auto tg) {
     constexpr int TG = decltype(tg)::value;
-    if (len == ADAMC_CHUNK) adamw_clip_chunk<TG, true>(a, t, off, len, factor, decay);
-    else adamw_clip_chunk<TG, false>(a, t, off, len, factor, decay);
+    if (len == CHUNK) adamw_clip_chunk<TG, CHUNK, true>(a, t, off, len, factor, decay);
+    else adamw_clip_chunk<TG, CHUNK, false>(a, t, off, len, factor, decay);
   });
 }
 
 hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s) {
   if (a.items == 0) return hipSuccess;
-  adamw_clip_kernel<<<a.items, GRAD_THREADS, 0, s>>>(a);
+  if (a.chunk == ADAMC_LONG_CHUNK)
+    adamw_clip_kernel<ADAMC_LONG_CHUNK><<<a.items, GRAD_THREADS, 0, s>>>(a);
+  else
+    adamw_clip_kernel<ADAMC_CHUNK><<<a.items, GRAD_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -4,6 +4,7 @@
 // with the host compiler under AddressSanitizer and
 // UndefinedBehaviorSanitizer by tests/test_grad_host.py.  Prints "ok" and
 // exits 0 when every check holds.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -58,7 +59,7 @@ struct List {
 static List make_list(int n, int decays) {
   List l;
   uintptr_t a = (uintptr_t)1 << 32;
-  auto next = [&] { a += (uintptr_t)1 << 24; return a + 4; };
+  auto next = [&] { a += (uintptr_t)1 << 26; return a + 4; };
   for (int i = 0; i < n; ++i) {
     l.numel.push_back(kSizes[(i * 7 + i / 13) % (sizeof kSizes / sizeof *kSizes)]);
     l.type.push_back(i % 3);
@@ -99,11 +100,16 @@ static int64_t covered(std::vector<std::pair<int64_t, int>> v) {
   return end;
 }
 
-static void check_norm(const List& l) {
-  const std::vector<NormArgs> a = norm_launches(l.g.data(), l.numel.data(), l.type.data(), l.n());
+static void check_norm(const List& l, int64_t keep) {
+  const std::vector<NormArgs> a = norm_launches(l.g.data(), l.numel.data(), l.type.data(), l.n(), keep);
   CHECK(!a.empty() && a.front().first == 1 && a.back().last == 1);
   std::map<const void*, int64_t> got;
+  int64_t items = 0, kept = 0;
   for (size_t k = 0; k < a.size(); ++k) {
+    CHECK(a[k].keep_from >= 0 && a[k].keep_from <= a[k].start[a[k].n]);
+    CHECK(k == 0 || a[k].keep_from == 0 || a[k - 1].keep_from == a[k - 1].start[a[k - 1].n]);  // the list's end
+    items += a[k].start[a[k].n];
+    kept += a[k].start[a[k].n] - a[k].keep_from;
     CHECK(a[k].first == (k == 0) && a[k].last == (k + 1 == a.size()));
     CHECK(a[k].blocks == a[0].blocks && a[k].blocks >= 1 && a[k].blocks <= NORM_MAX_BLOCKS);
     CHECK(a[k].n <= NORM_TENSORS);
@@ -113,6 +119,7 @@ static void check_norm(const List& l) {
            [&](int t) { return norm_chunk(a[k].tail[t] & 3); }, &seen);
     for (auto& s : seen) got[a[k].p[s.first]] += covered(s.second);
   }
+  CHECK(kept == std::min(items, keep / NORM_CHUNK_BYTES));
   size_t full = 0;
   for (int i = 0; i < l.n(); ++i) {
     if (l.numel[i] == 0) continue;
@@ -140,12 +147,15 @@ static void check_clip(const List& l) {
 }
 
 static void check_adamw(const List& l, bool with_wd) {
+  int64_t total = 0;
+  for (int64_t m : l.numel) total += m;
   std::map<const void*, int64_t> got;
   for (const AdamClipArgs& a : adamw_clip_launches(l.p.data(), l.g.data(), l.type.data(), l.u.data(), l.v.data(),
                                                    l.numel.data(), with_wd ? l.wd.data() : nullptr, l.n())) {
     CHECK(a.n >= 1 && a.n <= ADAMC_TENSORS && a.items == a.start[a.n]);
+    CHECK(a.chunk == (total >= ADAMC_LONG_MIN ? ADAMC_LONG_CHUNK : ADAMC_CHUNK));
     std::map<int, std::vector<std::pair<int64_t, int>>> seen;
-    walk(a.start, a.n, 0, 1, [&](int t) { return (int)(a.tail[t] >> 4); }, [](int) { return ADAMC_CHUNK; }, &seen);
+    walk(a.start, a.n, 0, 1, [&](int t) { return (int)(a.tail[t] >> 4); }, [&](int) { return a.chunk; }, &seen);
     for (auto& s : seen) {
       const int t = s.first;
       got[a.p[t]] += covered(s.second);
@@ -253,12 +263,19 @@ int main() {
     for (int decays : {1, 4, 5, 9}) {
       const List l = make_list(n, decays);
       if (decays == 1) {
-        check_norm(l);
+        for (int64_t keep : {(int64_t)0, (int64_t)1 << 20, NORM_KEEP_BYTES}) check_norm(l, keep);
         check_clip(l);
       }
       check_adamw(l, true);
       check_adamw(l, false);
     }
+  }
+  // a call long enough for the long chunks
+  {
+    List l = make_list(130, 3);
+    for (int i = 0; i < 130; ++i) l.numel[i] += (int64_t)1 << 20;
+    check_adamw(l, true);
+    check_norm(l, NORM_KEEP_BYTES);
   }
   // five decays in turn need a launch per four; grouped, as many as fit one
   {
@@ -276,7 +293,7 @@ int main() {
     std::vector<void*> o(20);
     for (int i = 0; i < 20; ++i) g[i] = o[i] = (void*)((uintptr_t)(i + 1) << 44);
     int64_t items = 0;
-    for (const NormArgs& a : norm_launches(g.data(), numel.data(), type.data(), 20)) {
+    for (const NormArgs& a : norm_launches(g.data(), numel.data(), type.data(), 20, NORM_KEEP_BYTES)) {
       CHECK(a.start[a.n] <= MAX_LAUNCH_ITEMS && a.start[a.n] >= 0);
       items += a.start[a.n];
     }

@@ -98,6 +98,27 @@ def test_adamw_many_tensors_and_decays(count, decays):
     _adamw_check(ts, record.cpu().numpy()[1], 1e-3, (0.9, 0.999), 1e-8, wds, 1)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_adamw_long_call(kind):
+    """A call of more than 2^27 elements (long chunks): equal to the unclipped
+    step on gradients multiplied beforehand."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    gen = torch.Generator(device="cuda").manual_seed(69)
+    sizes = [2 ** 27 + 4097, 8191, 8192, 8193, 3]
+    say(f"[adamw long] {kind}")
+    P, U, V, G = ([torch.randn(n, generator=gen, device="cuda") for n in sizes] for _ in "PUVG")
+    V = [v.square_() for v in V]
+    G = [g.to(_dtype(kind)) for g in G]
+    record = mu.muon_grad_norm(G, 100.0)
+    Pe, Ue, Ve = ([t.clone() for t in L] for L in (P, U, V))
+    wds = [0.1, 0.0, 0.1, 0.3, 0.2]
+    mu.muon_adamw_step(P, G, U, V, 1e-3, weight_decay=wds, step=3, clip=record)
+    mu.muon_adamw_step(Pe, [g.float() * record[1] for g in G], Ue, Ve, 1e-3, weight_decay=wds, step=3)
+    assert all(torch.equal(a, b) for a, b in zip(P + U + V, Pe + Ue + Ve))
+    assert record[1].item() < 0.1
+
+
 def test_adamw_without_a_record():
     """16-bit gradients as they are; fp32 ones under a factor of 1 give the
     plain step's bits."""
