@@ -47,7 +47,8 @@ def _check(rc: int) -> None:
 def _stream_handle(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # what torch.cuda.current_stream().cuda_stream gives, 2.8 us sooner
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -269,8 +270,7 @@ def _norm_buffers(record):
     A captured call takes a workspace of its own from the graph's memory,
     cleared by the graph, so that graphs share none either."""
     import torch
-    st = torch.cuda.current_stream()
-    handle, dev = st.cuda_stream, st.device
+    handle, dev = _stream_handle(None), torch.cuda.current_device()
     if record is None:
         record = torch.empty(2, dtype=torch.float32, device=dev)
     else:
@@ -279,9 +279,9 @@ def _norm_buffers(record):
         ws = torch.empty(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
         ws[:8].zero_()
         return record, ws, handle
-    ws = _norm_workspaces.get((dev.index, handle))
+    ws = _norm_workspaces.get((dev, handle))
     if ws is None:
-        ws = _norm_workspaces[dev.index, handle] = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
+        ws = _norm_workspaces[dev, handle] = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
     return record, ws, handle
 
 

@@ -87,10 +87,7 @@ def load_tensor_args():
 
 
 def ptr_array(ptrs):
-    arr = (ctypes.c_void_p * max(1, len(ptrs)))()
-    for i, p in enumerate(ptrs):
-        arr[i] = p
-    return arr
+    return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
 
 
 def shape_array(shapes):
@@ -109,14 +106,8 @@ def float3(vals):
 
 
 def float_array(vals):
-    arr = (ctypes.c_float * max(1, len(vals)))()
-    for i, v in enumerate(vals):
-        arr[i] = float(v)
-    return arr
+    return (ctypes.c_float * max(1, len(vals)))(*map(float, vals))
 
 
 def int64_array(vals):
-    arr = (ctypes.c_int64 * max(1, len(vals)))()
-    for i, v in enumerate(vals):
-        arr[i] = int(v)
-    return arr
+    return (ctypes.c_int64 * max(1, len(vals)))(*map(int, vals))

@@ -208,6 +208,7 @@ std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* num
   }
   int32_t most = 1;
   for (const NormArgs& a : out) most = std::max(most, a.start[a.n]);
+  if (out.size() == 1 && most <= NORM_SMALL_ITEMS) most = 1;
   for (NormArgs& a : out) a.blocks = std::min(most, (int32_t)NORM_MAX_BLOCKS);
   return out;
 }

@@ -38,6 +38,10 @@ constexpr int NORM_MAX_BLOCKS = 1024;    // partial sums in the workspace
 // and 196 us, of 124 M 686 and 642 us; norm and clip of 124 M bf16 elements
 // into fp32 170 and 155 us.
 constexpr int64_t NORM_KEEP_BYTES = (int64_t)256 << 20;
+// A call of at most NORM_SMALL_ITEMS items is one block, a wave to an item,
+// and needs no arrivals.
+constexpr int NORM_SMALL_ITEMS = 16;
+constexpr int NORM_SMALL_THREADS = 1024;
 constexpr int NORM_GROUP = 32;           // blocks that count on one counter
 constexpr int NORM_MAX_GROUPS = NORM_MAX_BLOCKS / NORM_GROUP;
 constexpr int norm_chunk(int type) { return NORM_CHUNK_BYTES / grad_type_bytes(type); }

@@ -24,6 +24,7 @@ namespace {
 constexpr int kWavesG = GRAD_THREADS / 64;
 
 // Fixed-order block sum of one double per thread, valid in thread 0.
+template <int WAVES>
 __device__ __forceinline__ double block_sum_f64(double v, double* red) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
@@ -32,24 +33,25 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red) {
   double s = 0.0;
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int w = 0; w < kWavesG; ++w) s += red[w];
+    for (int w = 0; w < WAVES; ++w) s += red[w];
   }
   return s;
 }
 
-// Sum of squares of this thread's elements of one chunk of len elements; all
-// its loads go out before the first square.  A partial chunk's vectors that
-// fit are loaded whole, the up to 7 elements behind them one per thread.
-template <int TYPE, bool FULL, bool KEEP>
-__device__ __forceinline__ double chunk_squares(const void* base, int64_t off, int len) {
+// Sum of squares of this thread's elements (thread tid of THREADS) of one
+// chunk of len elements; all its loads go out before the first square.  A
+// partial chunk's vectors that fit are loaded whole, the up to 7 elements
+// behind them one per thread.
+template <int TYPE, bool FULL, bool KEEP, int THREADS>
+__device__ __forceinline__ double chunk_squares(const void* base, int64_t off, int len, int tid) {
   typedef Elem<TYPE> E;
   constexpr int E16 = 16 / grad_type_bytes(TYPE);  // elements of a 16-byte load
-  constexpr int V = norm_chunk(TYPE) / (E16 * GRAD_THREADS);
+  constexpr int V = norm_chunk(TYPE) / (E16 * THREADS);
   const MUON_GLOBAL typename E::scalar* g = gptr(static_cast<const typename E::scalar*>(base)) + off;
   typename E::wide w[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int e = E16 * (k * GRAD_THREADS + threadIdx.x);
+    const int e = E16 * (k * THREADS + tid);
     if (FULL || e + E16 <= len)
       w[k] = KEEP ? *reinterpret_cast<const MUON_GLOBAL typename E::wide*>(g + e)
                   : __builtin_nontemporal_load(reinterpret_cast<const MUON_GLOBAL typename E::wide*>(g + e));
@@ -57,8 +59,8 @@ __device__ __forceinline__ double chunk_squares(const void* base, int64_t off, i
       w[k] = typename E::wide(0);
   }
   double s = 0.0;
-  if (!FULL && (int)threadIdx.x < len % E16) {
-    const double v = E::widen1(g[len - len % E16 + threadIdx.x]);
+  if (!FULL && tid < len % E16) {
+    const double v = E::widen1(g[len - len % E16 + tid]);
     s = v * v;
   }
 #pragma unroll
@@ -69,6 +71,16 @@ __device__ __forceinline__ double chunk_squares(const void* base, int64_t off, i
       s += v * v;
     }
   return s;
+}
+
+// The record of a call's sum of squares.
+__device__ __forceinline__ void write_record(const NormArgs& a, double sum) {
+  const double norm = (double)a.scale * sqrt(sum);
+  double c = 1.0;
+  if (isnan(norm)) c = norm;
+  else if (!isinf(a.max_norm)) c = fmin(1.0, (double)a.max_norm / (norm + 1e-6));
+  a.record[0] = (float)norm;
+  a.record[1] = (float)(a.scale * c);
 }
 
 // The block's items from it up to end; it and t (its tensor) move on.
@@ -83,8 +95,8 @@ __device__ __forceinline__ double sum_items(const NormArgs& a, int end, int& it,
     with_type(tail & 3, [&](auto tag) {
       constexpr int TYPE = decltype(tag)::value, CH = norm_chunk(TYPE);
       const int len = ends ? (int)(tail >> 2) : CH;
-      if (len == CH) s += chunk_squares<TYPE, true, KEEP>(a.p[t], c * CH, CH);
-      else s += chunk_squares<TYPE, false, KEEP>(a.p[t], c * CH, len);
+      if (len == CH) s += chunk_squares<TYPE, true, KEEP, GRAD_THREADS>(a.p[t], c * CH, CH, threadIdx.x);
+      else s += chunk_squares<TYPE, false, KEEP, GRAD_THREADS>(a.p[t], c * CH, len, threadIdx.x);
     });
   }
   return s;
@@ -134,7 +146,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_norm_kernel(const NormArgs 
   int it = blockIdx.x, t = 0;
   double s = sum_items<false>(a, min(items, a.keep_from), it, t);
   s += sum_items<true>(a, items, it, t);
-  s = block_sum_f64(s, red);
+  s = block_sum_f64<kWavesG>(s, red);
   NormWorkspace* ws = a.ws;
   if (threadIdx.x == 0) {
     if (!a.first) s += ws->part[blockIdx.x];
@@ -146,15 +158,30 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_norm_kernel(const NormArgs 
   s = 0.0;
   for (int k = threadIdx.x; k < a.blocks; k += GRAD_THREADS)
     s += __hip_atomic_load(&ws->part[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  s = block_sum_f64(s, red);
-  if (threadIdx.x == 0) {
-    const double norm = (double)a.scale * sqrt(s);
-    double c = 1.0;
-    if (isnan(norm)) c = norm;
-    else if (!isinf(a.max_norm)) c = fmin(1.0, (double)a.max_norm / (norm + 1e-6));
-    a.record[0] = (float)norm;
-    a.record[1] = (float)(a.scale * c);
+  s = block_sum_f64<kWavesG>(s, red);
+  if (threadIdx.x == 0) write_record(a, s);
+}
+
+// A call of at most NORM_SMALL_ITEMS items in one block, wave w taking items
+// w, w + waves, ...: no partials in memory and no arrivals, whose three trips to memory are
+// most of a small call's time.
+__global__ __launch_bounds__(NORM_SMALL_THREADS) void grad_norm_small_kernel(const NormArgs a) {
+  constexpr int kWaves = NORM_SMALL_THREADS / 64;
+  __shared__ double red[kWaves];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  double s = 0.0;
+  for (int it = wave; it < a.start[a.n]; it += kWaves) {
+    const int t = find_tensor(a.start, 0, a.n, it);
+    const uint32_t tail = a.tail[t];
+    const int64_t c = it - a.start[t];
+    const bool ends = it + 1 == a.start[t + 1];
+    with_type(tail & 3, [&](auto tag) {
+      constexpr int TYPE = decltype(tag)::value, CH = norm_chunk(TYPE);
+      s += chunk_squares<TYPE, false, true, 64>(a.p[t], c * CH, ends ? (int)(tail >> 2) : CH, lane);
+    });
   }
+  s = block_sum_f64<kWaves>(s, red);
+  if (threadIdx.x == 0) write_record(a, s);
 }
 
 namespace {
@@ -221,7 +248,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(const ClipArgs 
 }
 
 hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s) {
-  grad_norm_kernel<<<a.blocks, GRAD_THREADS, 0, s>>>(a);
+  if (a.blocks == 1)
+    grad_norm_small_kernel<<<1, NORM_SMALL_THREADS, 0, s>>>(a);
+  else
+    grad_norm_kernel<<<a.blocks, GRAD_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 
