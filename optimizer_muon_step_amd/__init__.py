@@ -224,12 +224,16 @@ def _as_list(ts):
     return ts if isinstance(ts, (list, tuple)) else list(ts)
 
 
-def _flat_list(ts, what, any_type, dense):
-    """(addresses, element counts, type codes) of a list of tensors taken flat, as C arrays."""
+def _check_device(what, dev):
     import torch
-    ptrs, numels, types, dev = _lib.load_tensor_args().flat(ts, what, any_type, dense)
     if dev >= 0 and dev != torch.cuda.current_device():
         raise ValueError(f"{what}: tensors on GPU {dev}, the current one is {torch.cuda.current_device()}")
+
+
+def _flat_list(ts, what, any_type, dense):
+    """(addresses, element counts, type codes) of a list of tensors taken flat, as C arrays."""
+    ptrs, numels, types, dev = _lib.load_tensor_args().flat(ts, what, any_type, dense)
+    _check_device(what, dev)
     return ptrs, numels, types
 
 
@@ -297,11 +301,11 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
     if not (len(grads) == len(exp_avg) == len(exp_avg_sq) == n):
         raise ValueError("params, grads, exp_avg and exp_avg_sq must have the same length")
     if hasattr(weight_decay, "__len__"):
-        wds = [float(w) for w in weight_decay]
-        if len(wds) != n:
+        if len(weight_decay) != n:
             raise ValueError("weight_decay: expected one value or one per tensor")
+        wds = _lib.float_array(weight_decay)
     else:
-        wds = [float(weight_decay)] * n
+        wds = _lib.float_array([weight_decay] * n)
     if clip is not None or _any_16_bit(grads):
         return _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip)
     ptrs = ([], [], [], [])
@@ -316,24 +320,28 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
         numels.append(params[i].numel())
     b1, b2 = betas
     rc = _lib.load().muon_adamw_step(*(_lib.ptr_array(p) for p in ptrs), _lib.int64_array(numels),
-                                     _lib.float_array(wds), n, float(lr), float(b1), float(b2), float(eps),
+                                     wds, n, float(lr), float(b1), float(b2), float(eps),
                                      int(step), ctypes.c_void_p(_stream_handle(stream)))
     _check(rc)
 
 
 def _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip):
     n = len(params)
-    lists = [_flat_list(ts, what, any_type=what == "grads", dense=False)
-             for ts, what in ((params, "params"), (grads, "grads"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"))]
-    (p, numels, _), (g, g_numels, types), (u, u_numels, _), (v, v_numels, _) = lists
+    flat = _lib.load_tensor_args().flat
+    p, numels, _, dev = flat(params, "params", False, False)
+    g, g_numels, types, g_dev = flat(grads, "grads", True, False)
+    u, u_numels, _, u_dev = flat(exp_avg, "exp_avg", False, False)
+    v, v_numels, _, v_dev = flat(exp_avg_sq, "exp_avg_sq", False, False)
+    if not dev == g_dev == u_dev == v_dev:
+        raise ValueError(f"params, grads, exp_avg and exp_avg_sq on GPUs {dev}, {g_dev}, {u_dev} and {v_dev}")
+    _check_device("params", dev)
     if not numels == g_numels == u_numels == v_numels:
         i = next(i for i in range(n) if len({ts[i].numel() for ts in (params, grads, exp_avg, exp_avg_sq)}) != 1)
         raise ValueError(f"tensor {i}: element counts differ")
     record = None if clip is None else _record_ptr(clip)
-    _check(_lib.load().muon_adamw_step_clip(p, g, types, u, v,
-                                            numels, _lib.float_array(wds), n, float(lr),
-                                            float(betas[0]), float(betas[1]), float(eps), int(step), record,
-                                            _stream_handle(stream)))
+    b1, b2 = betas
+    _check(_lib.load().muon_adamw_step_clip(p, g, types, u, v, numels, wds, n, float(lr), float(b1), float(b2),
+                                            float(eps), int(step), record, _stream_handle(stream)))
 
 
 def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=None):

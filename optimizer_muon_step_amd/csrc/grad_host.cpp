@@ -88,6 +88,11 @@ Cut cut_of(int64_t numel, int chunk) {
   return {items, (uint32_t)(numel - (items - 1) * chunk)};
 }
 
+template <typename Args>
+void fill_unused(Args& a) {
+  std::fill(a.start + a.n + 1, a.start + sizeof a.start / sizeof *a.start, START_UNUSED);
+}
+
 }  // namespace
 
 int validate_grad_norm(const void* const* grads, const int64_t* numels, const int* types, int n, float max_norm,
@@ -189,25 +194,26 @@ std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* num
     if (numels[i] == 0) continue;
     const Cut c = cut_of(numels[i], norm_chunk(types[i]));
     NormArgs* a = &out.back();
-    if (a->n == NORM_TENSORS || (a->n > 0 && a->start[a->n] + c.items > MAX_LAUNCH_ITEMS)) {
+    if (a->n == NORM_TENSORS || (a->n > 0 && a->items + c.items > MAX_LAUNCH_ITEMS)) {
       out.push_back(NormArgs{});
       a = &out.back();
     }
     a->tail[a->n] = c.last << 2 | (uint32_t)types[i];
     a->p[a->n] = grads[i];
-    a->start[a->n + 1] = a->start[a->n] + (int32_t)c.items;
-    ++a->n;
+    a->items += (int32_t)c.items;
+    a->start[++a->n] = a->items;
   }
+  for (NormArgs& a : out) fill_unused(a);
   out.front().first = 1;
   out.back().last = 1;
   int64_t left = keep_bytes;
   for (auto a = out.rbegin(); a != out.rend(); ++a) {
-    const int64_t items = std::min<int64_t>(a->start[a->n], left / NORM_CHUNK_BYTES);
-    a->keep_from = a->start[a->n] - (int32_t)items;
+    const int64_t items = std::min<int64_t>(a->items, left / NORM_CHUNK_BYTES);
+    a->keep_from = a->items - (int32_t)items;
     left -= items * NORM_CHUNK_BYTES;
   }
   int32_t most = 1;
-  for (const NormArgs& a : out) most = std::max(most, a.start[a.n]);
+  for (const NormArgs& a : out) most = std::max(most, a.items);
   if (out.size() == 1 && most <= NORM_SMALL_ITEMS) most = 1;
   for (NormArgs& a : out) a.blocks = std::min(most, (int32_t)NORM_MAX_BLOCKS);
   return out;
@@ -231,6 +237,7 @@ std::vector<ClipArgs> clip_launches(const void* const* grads, void* const* outs,
     a.items += (int32_t)c.items;
     a.start[++a.n] = a.items;
   }
+  for (auto& a : out) fill_unused(a);
   return out;
 }
 
@@ -265,6 +272,7 @@ std::vector<AdamClipArgs> adamw_clip_launches(float* const* params, const void* 
     a.items += (int32_t)c.items;
     a.start[++a.n] = a.items;
   }
+  for (auto& a : out) fill_unused(a);
   return out;
 }
 

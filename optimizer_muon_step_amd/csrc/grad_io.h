@@ -1,5 +1,5 @@
 // Gradient elements of the three types on gfx950: typed loads and stores of
-// four at a time, and the search for a block's tensor in a launch's table.
+// four at a time, and the search for an item's tensor in a launch's table.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -77,16 +77,34 @@ struct Elem<GRAD_FP16> {
   }
 };
 
-// The tensor that owns item: start[t] <= item < start[t + 1], t in [lo, n).
-// item is uniform over the block, so this is scalar code.
-__device__ __forceinline__ int find_tensor(const int32_t* start, int lo, int n, int item) {
-  int hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= item) lo = mid; else hi = mid;
+// The tensor that owns a work item, from a launch's table of first items
+// (ascending from 0; START_UNUSED behind the last entry).  A wave holds the
+// table in registers, so a search costs one trip to the kernel arguments and
+// not one for each step of a bisection (norm of 61 tensors, 833 items: 8.6 -> 7.7 us).
+// Every lane of the wave takes part; item is uniform over it.
+template <int ENTRIES>
+struct TensorFinder {
+  static constexpr int K = (ENTRIES + 63) / 64;
+  int32_t s[K];
+  __device__ __forceinline__ explicit TensorFinder(const int32_t* start) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = k * 64 + lane < ENTRIES ? start[k * 64 + lane] : START_UNUSED;
   }
-  return lo;
-}
+  // t with start[t] <= item < start[t + 1].
+  __device__ __forceinline__ int operator()(int item) const {
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) c += __popcll(__ballot(s[k] <= item));
+    return c - 1;
+  }
+  __device__ __forceinline__ int start_of(int t) const {
+    int r = __builtin_amdgcn_readlane(s[0], t & 63);
+#pragma unroll
+    for (int k = 1; k < K; ++k) r = t >> 6 == k ? __builtin_amdgcn_readlane(s[k], t & 63) : r;
+    return r;
+  }
+};
 
 // f(Tag<type>) for a run-time element type.
 template <int T>

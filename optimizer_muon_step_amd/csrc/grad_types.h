@@ -21,9 +21,11 @@ constexpr int grad_type_bytes(int t) { return t == GRAD_FP32 ? 4 : 2; }
 
 // Work items of a launch are chunks of its tensors: tensor t owns items
 // start[t] .. start[t + 1] - 1, all of the full chunk length except the last,
-// whose elements are counted in tail[t] (shifted past the type bits).  A grid
+// whose elements are counted in tail[t] (shifted past the type bits); start
+// holds START_UNUSED behind start[n].  A grid
 // holds fewer than 2^32 threads, so a launch of one block per item takes
 // fewer than 2^24 items.
+constexpr int32_t START_UNUSED = INT32_MAX;
 constexpr int64_t MAX_LAUNCH_ITEMS = (1 << 24) - 1;
 constexpr int64_t GRAD_MAX_NUMEL = (int64_t)1 << 35;
 
@@ -60,18 +62,21 @@ struct NormWorkspace {
 };
 
 constexpr int NORM_TENSORS = (KERNARG_BYTES - 64) / 16;
-struct NormArgs {
+template <int TENSORS>
+struct NormTable {
   NormWorkspace* ws;
   float* record;        // {norm, factor}
   float max_norm, scale;
-  int32_t n;            // tensors of this launch
+  int32_t n, items;     // tensors and work items of this launch
   int32_t blocks;       // grid of every launch of the call
   int32_t first, last;  // first / last launch of the call
   int32_t keep_from;    // items from here on are read so as to stay in the memory-side cache
-  int32_t start[NORM_TENSORS + 1];
-  uint32_t tail[NORM_TENSORS];  // elements of the last chunk << 2 | type
-  const void* p[NORM_TENSORS];
+  int32_t start[TENSORS + 1];
+  uint32_t tail[TENSORS];  // elements of the last chunk << 2 | type
+  const void* p[TENSORS];
 };
+typedef NormTable<NORM_TENSORS> NormArgs;
+typedef NormTable<NORM_SMALL_ITEMS> NormSmallArgs;
 static_assert(sizeof(NormArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // ---- clipping ----
@@ -99,10 +104,13 @@ struct ClipArgs {
 static_assert(sizeof(ClipArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // ---- AdamW on clipped gradients ----
-// Elements per work item: long chunks for calls of at least ADAMC_LONG_MIN
-// elements (1.56 G elements with bf16 gradients 7.62 -> 7.28 ms with the
-// norm, 124 M fp32 alike, 39.5 M fp32 196 -> 201 us: fewer, larger blocks end less evenly).
+// Elements per work item: long chunks, in per-XCD runs of ADAMC_LONG_RUN, for
+// calls of at least ADAMC_LONG_MIN elements.  Measured with short and with
+// long chunks, norm included: 1.56 G elements with bf16 gradients 7.62 and
+// 7.45 ms (7.22 in runs), 124 M fp32 642 and 636 us (runs 647), 39.5 M fp32 196 and 201 us
+// (fewer, larger blocks end less evenly).
 constexpr int ADAMC_CHUNK = 4096, ADAMC_LONG_CHUNK = 8192;
+constexpr int ADAMC_LONG_RUN = 16;
 constexpr int64_t ADAMC_LONG_MIN = (int64_t)1 << 27;
 constexpr int ADAMC_DECAYS = 4;    // distinct weight decays of a launch
 constexpr int ADAMC_TENSORS = (KERNARG_BYTES - 80) / 40;

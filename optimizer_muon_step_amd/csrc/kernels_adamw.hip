@@ -170,17 +170,18 @@ __device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, i
 // the device.  A norm that is not finite leaves everything as it was.
 template <int CHUNK>
 __global__ __launch_bounds__(GRAD_THREADS) void adamw_clip_kernel(const AdamClipArgs a) {
+  const int it = CHUNK == ADAMC_LONG_CHUNK ? ew_item_of_block(blockIdx.x, a.items, ADAMC_LONG_RUN) : blockIdx.x;
+  const grad::TensorFinder<ADAMC_TENSORS + 1> find(a.start);
+  const int t = find(it);
+  const uint32_t tail = a.tail[t];
+  const int64_t off = (int64_t)(it - find.start_of(t)) * CHUNK;
+  const int len = find(it + 1) != t ? (int)(tail >> 4) : CHUNK;
+  const float decay = 1.0f - a.lr * a.wd[(tail >> 2) & 3];
   float factor = 1.0f;
   if (a.record) {
     factor = a.record[1];
     if (!isfinite(a.record[0])) return;
   }
-  const int it = blockIdx.x;
-  const int t = grad::find_tensor(a.start, 0, a.n, it);
-  const uint32_t tail = a.tail[t];
-  const int64_t off = (int64_t)(it - a.start[t]) * CHUNK;
-  const int len = it + 1 == a.start[t + 1] ? (int)(tail >> 4) : CHUNK;
-  const float decay = 1.0f - a.lr * a.wd[(tail >> 2) & 3];
   grad::with_type(tail & 3, [&](auto tg) {
     constexpr int TG = decltype(tg)::value;
     if (len == CHUNK) adamw_clip_chunk<TG, CHUNK, true>(a, t, off, len, factor, decay);

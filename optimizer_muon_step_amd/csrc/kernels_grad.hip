@@ -11,6 +11,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "bf16_util.h"
 #include "grad_io.h"
 #include "muon_internal.h"
@@ -74,24 +76,26 @@ __device__ __forceinline__ double chunk_squares(const void* base, int64_t off, i
 }
 
 // The record of a call's sum of squares.
-__device__ __forceinline__ void write_record(const NormArgs& a, double sum) {
-  const double norm = (double)a.scale * sqrt(sum);
+__device__ __forceinline__ void write_record(float* record, float max_norm, float scale, double sum) {
+  const double norm = (double)scale * sqrt(sum);
   double c = 1.0;
   if (isnan(norm)) c = norm;
-  else if (!isinf(a.max_norm)) c = fmin(1.0, (double)a.max_norm / (norm + 1e-6));
-  a.record[0] = (float)norm;
-  a.record[1] = (float)(a.scale * c);
+  else if (!isinf(max_norm)) c = fmin(1.0, (double)max_norm / (norm + 1e-6));
+  record[0] = (float)norm;
+  record[1] = (float)(scale * c);
 }
 
-// The block's items from it up to end; it and t (its tensor) move on.
+typedef TensorFinder<NORM_TENSORS + 1> NormFinder;
+
+// The block's items from it up to end; it moves on.
 template <bool KEEP>
-__device__ __forceinline__ double sum_items(const NormArgs& a, int end, int& it, int& t) {
+__device__ __forceinline__ double sum_items(const NormArgs& a, const NormFinder& find, int end, int& it) {
   double s = 0.0;
   for (; it < end; it += a.blocks) {
-    t = find_tensor(a.start, t, a.n, it);
+    const int t = find(it);
     const uint32_t tail = a.tail[t];
-    const int64_t c = it - a.start[t];
-    const bool ends = it + 1 == a.start[t + 1];
+    const int64_t c = it - find.start_of(t);
+    const bool ends = find(it + 1) != t;
     with_type(tail & 3, [&](auto tag) {
       constexpr int TYPE = decltype(tag)::value, CH = norm_chunk(TYPE);
       const int len = ends ? (int)(tail >> 2) : CH;
@@ -142,10 +146,11 @@ __device__ __forceinline__ bool last_arrival(NormWorkspace* ws, int blocks) {
 __global__ __launch_bounds__(GRAD_THREADS) void grad_norm_kernel(const NormArgs a) {
   __shared__ double red[kWavesG];
   __shared__ int is_last;
-  const int items = a.start[a.n];
-  int it = blockIdx.x, t = 0;
-  double s = sum_items<false>(a, min(items, a.keep_from), it, t);
-  s += sum_items<true>(a, items, it, t);
+  const int items = a.items;
+  const NormFinder find(a.start);
+  int it = blockIdx.x;
+  double s = sum_items<false>(a, find, min(items, a.keep_from), it);
+  s += sum_items<true>(a, find, items, it);
   s = block_sum_f64<kWavesG>(s, red);
   NormWorkspace* ws = a.ws;
   if (threadIdx.x == 0) {
@@ -159,29 +164,30 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_norm_kernel(const NormArgs 
   for (int k = threadIdx.x; k < a.blocks; k += GRAD_THREADS)
     s += __hip_atomic_load(&ws->part[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   s = block_sum_f64<kWavesG>(s, red);
-  if (threadIdx.x == 0) write_record(a, s);
+  if (threadIdx.x == 0) write_record(a.record, a.max_norm, a.scale, s);
 }
 
 // A call of at most NORM_SMALL_ITEMS items in one block, wave w taking items
 // w, w + waves, ...: no partials in memory and no arrivals, whose three trips to memory are
 // most of a small call's time.
-__global__ __launch_bounds__(NORM_SMALL_THREADS) void grad_norm_small_kernel(const NormArgs a) {
+__global__ __launch_bounds__(NORM_SMALL_THREADS) void grad_norm_small_kernel(const NormSmallArgs a) {
   constexpr int kWaves = NORM_SMALL_THREADS / 64;
   __shared__ double red[kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   double s = 0.0;
-  for (int it = wave; it < a.start[a.n]; it += kWaves) {
-    const int t = find_tensor(a.start, 0, a.n, it);
+  const TensorFinder<NORM_SMALL_ITEMS + 1> find(a.start);
+  for (int it = wave; it < a.items; it += kWaves) {
+    const int t = find(it);
     const uint32_t tail = a.tail[t];
-    const int64_t c = it - a.start[t];
-    const bool ends = it + 1 == a.start[t + 1];
+    const int64_t c = it - find.start_of(t);
+    const bool ends = find(it + 1) != t;
     with_type(tail & 3, [&](auto tag) {
       constexpr int TYPE = decltype(tag)::value, CH = norm_chunk(TYPE);
       s += chunk_squares<TYPE, false, true, 64>(a.p[t], c * CH, ends ? (int)(tail >> 2) : CH, lane);
     });
   }
   s = block_sum_f64<kWaves>(s, red);
-  if (threadIdx.x == 0) write_record(a, s);
+  if (threadIdx.x == 0) write_record(a.record, a.max_norm, a.scale, s);
 }
 
 namespace {
@@ -229,14 +235,15 @@ __device__ __forceinline__ void clip_chunk(const void* in, void* out, int64_t of
 __global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(const ClipArgs a) {
   const float factor = a.record[1];
   if (a.in_place && factor == 1.0f) return;
+  const TensorFinder<CLIP_TENSORS + 1> find(a.start);
   const int blocks = clip_blocks(a);
   for (int b = blockIdx.x; b < a.items; b += blocks) {
     const int it = a.in_place ? b : ew_item_of_block(b, a.items, CLIP_RUN);
-    const int t = find_tensor(a.start, 0, a.n, it);
-    if (factor == 1.0f && a.in[t] == a.out[t]) continue;
+    const int t = find(it);
+    if (a.in[t] == a.out[t] && factor == 1.0f) continue;
     const uint32_t tail = a.tail[t];
-    const int64_t off = (int64_t)(it - a.start[t]) * CLIP_CHUNK;
-    const int len = it + 1 == a.start[t + 1] ? (int)(tail >> 4) : CLIP_CHUNK;
+    const int64_t off = (int64_t)(it - find.start_of(t)) * CLIP_CHUNK;
+    const int len = find(it + 1) != t ? (int)(tail >> 4) : CLIP_CHUNK;
     with_type(tail & 3, [&](auto ti) {
       with_type((tail >> 2) & 3, [&](auto to) {
         constexpr int TI = decltype(ti)::value, TO = decltype(to)::value;
@@ -248,10 +255,20 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(const ClipArgs 
 }
 
 hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s) {
-  if (a.blocks == 1)
-    grad_norm_small_kernel<<<1, NORM_SMALL_THREADS, 0, s>>>(a);
-  else
+  if (a.blocks == 1) {
+    NormSmallArgs b{};
+    b.record = a.record;
+    b.max_norm = a.max_norm;
+    b.scale = a.scale;
+    b.n = a.n;
+    b.items = a.items;
+    std::copy_n(a.start, NORM_SMALL_ITEMS + 1, b.start);
+    std::copy_n(a.tail, a.n, b.tail);
+    std::copy_n(a.p, a.n, b.p);
+    grad_norm_small_kernel<<<1, NORM_SMALL_THREADS, 0, s>>>(b);
+  } else {
     grad_norm_kernel<<<a.blocks, GRAD_THREADS, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -33,14 +33,11 @@ static bool refused(int rc, const char* text) {
   return ok;
 }
 
-// The kernels' search (grad_io.h).
-static int find_tensor(const int32_t* start, int lo, int n, int item) {
-  int hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= item) lo = mid; else hi = mid;
-  }
-  return lo;
+// The kernels' search (grad_io.h): entries at or below the item, of the whole table.
+static int find_tensor(const int32_t* start, int entries, int item) {
+  int c = 0;
+  for (int k = 0; k < entries; ++k) c += start[k] <= item;
+  return c - 1;
 }
 
 static const int64_t kSizes[] = {0, 1, 3, 64, 4095, 4096, 4097, 8191, 8192, 8193, 12288, 40000, 1 << 20};
@@ -76,13 +73,12 @@ static List make_list(int n, int decays) {
 
 // Walks the items of one launch: seen[p] = elements covered of the tensor at p, in order.
 template <typename Tail, typename Chunk>
-static void walk(const int32_t* start, int n, int first, int stride, Tail tail, Chunk chunk,
+static void walk(const int32_t* start, int entries, int n, int first, int stride, Tail tail, Chunk chunk,
                  std::map<int, std::vector<std::pair<int64_t, int>>>* seen) {
-  int t = 0;
   for (int it = first; it < start[n]; it += stride) {
-    t = find_tensor(start, t, n, it);
+    const int t = find_tensor(start, entries, it);
     CHECK(t >= 0 && t < n && start[t] <= it && it < start[t + 1]);
-    const int len = it + 1 == start[t + 1] ? tail(t) : chunk(t);
+    const int len = find_tensor(start, entries, it + 1) != t ? tail(t) : chunk(t);
     CHECK(len >= 1 && len <= chunk(t));
     (*seen)[t].push_back({(int64_t)(it - start[t]) * chunk(t), len});
   }
@@ -112,10 +108,10 @@ static void check_norm(const List& l, int64_t keep) {
     kept += a[k].start[a[k].n] - a[k].keep_from;
     CHECK(a[k].first == (k == 0) && a[k].last == (k + 1 == a.size()));
     CHECK(a[k].blocks == a[0].blocks && a[k].blocks >= 1 && a[k].blocks <= NORM_MAX_BLOCKS);
-    CHECK(a[k].n <= NORM_TENSORS);
+    CHECK(a[k].n <= NORM_TENSORS && a[k].items == a[k].start[a[k].n]);
     std::map<int, std::vector<std::pair<int64_t, int>>> seen;
     for (int b = 0; b < a[k].blocks; ++b)
-      walk(a[k].start, a[k].n, b, a[k].blocks, [&](int t) { return (int)(a[k].tail[t] >> 2); },
+      walk(a[k].start, NORM_TENSORS + 1, a[k].n, b, a[k].blocks, [&](int t) { return (int)(a[k].tail[t] >> 2); },
            [&](int t) { return norm_chunk(a[k].tail[t] & 3); }, &seen);
     for (auto& s : seen) got[a[k].p[s.first]] += covered(s.second);
   }
@@ -134,7 +130,7 @@ static void check_clip(const List& l) {
   for (const ClipArgs& a : clip_launches(l.g.data(), l.out.data(), l.numel.data(), l.type.data(), l.out_type.data(), l.n())) {
     CHECK(a.n >= 1 && a.n <= CLIP_TENSORS && a.items == a.start[a.n]);
     std::map<int, std::vector<std::pair<int64_t, int>>> seen;
-    walk(a.start, a.n, 0, 1, [&](int t) { return (int)(a.tail[t] >> 4); }, [](int) { return CLIP_CHUNK; }, &seen);
+    walk(a.start, CLIP_TENSORS + 1, a.n, 0, 1, [&](int t) { return (int)(a.tail[t] >> 4); }, [](int) { return CLIP_CHUNK; }, &seen);
     for (auto& s : seen) {
       got[a.out[s.first]] += covered(s.second);
       for (int i = 0; i < l.n(); ++i)
@@ -155,7 +151,7 @@ static void check_adamw(const List& l, bool with_wd) {
     CHECK(a.n >= 1 && a.n <= ADAMC_TENSORS && a.items == a.start[a.n]);
     CHECK(a.chunk == (total >= ADAMC_LONG_MIN ? ADAMC_LONG_CHUNK : ADAMC_CHUNK));
     std::map<int, std::vector<std::pair<int64_t, int>>> seen;
-    walk(a.start, a.n, 0, 1, [&](int t) { return (int)(a.tail[t] >> 4); }, [&](int) { return a.chunk; }, &seen);
+    walk(a.start, ADAMC_TENSORS + 1, a.n, 0, 1, [&](int t) { return (int)(a.tail[t] >> 4); }, [&](int) { return a.chunk; }, &seen);
     for (auto& s : seen) {
       const int t = s.first;
       got[a.p[t]] += covered(s.second);
