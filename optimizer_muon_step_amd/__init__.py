@@ -280,9 +280,7 @@ def _norm_buffers(record):
     else:
         _record_ptr(record)
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
-        ws[:8].zero_()
-        return record, ws, handle
+        return record, torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev), handle
     ws = _norm_workspaces.get((dev, handle))
     if ws is None:
         ws = _norm_workspaces[dev, handle] = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
@@ -356,11 +354,10 @@ def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=
     to fill instead of a new one."""
     grads = _as_list(grads)
     ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
-    lib = _lib.load()
     with _on_stream(stream):
         record, ws, st = _norm_buffers(record)
-        _check(lib.muon_grad_norm(ptrs, numels, types, len(grads), float(max_norm),
-                                  float(scale), record.data_ptr(), ws.data_ptr(), st))
+        _check(_lib.load().muon_grad_norm(ptrs, numels, types, len(grads), float(max_norm), float(scale),
+                                          record.data_ptr(), ws.data_ptr(), st))
     return record
 
 
@@ -382,12 +379,10 @@ def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=No
         i = _lib.load_tensor_args().first_unlike(grads, outs)
         if i >= 0:
             raise ValueError(f"outs[{i}]: shape or memory order differs from grads[{i}]")
-    lib = _lib.load()
     with _on_stream(stream):
         record, ws, st = _norm_buffers(record)
-        _check(lib.muon_grad_clip(ptrs, out_ptrs, numels, types,
-                                  out_types, len(grads), float(max_norm), float(scale), record.data_ptr(),
-                                  ws.data_ptr(), st))
+        _check(_lib.load().muon_grad_clip(ptrs, out_ptrs, numels, types, out_types, len(grads), float(max_norm),
+                                          float(scale), record.data_ptr(), ws.data_ptr(), st))
     return record
 
 

@@ -31,6 +31,17 @@ int enqueue_norm(std::vector<NormArgs>& launches, float max_norm, float scale, f
   return MUON_OK;
 }
 
+// The one launch of a small norm, or of a small clip with its norm (timed as
+// the clip).
+int enqueue_small(GradSmallArgs& a, bool clip, float max_norm, float scale, float* record, hipStream_t stream) {
+  a.record = record;
+  a.max_norm = max_norm;
+  a.scale = scale;
+  std::lock_guard<std::mutex> lock(api_mutex());
+  return timed(clip ? MUON_KERNEL_GRAD_CLIP : MUON_KERNEL_GRAD_NORM, stream,
+               [&] { return launch_grad_small(a, clip, stream); }, "gradient norm kernel launch");
+}
+
 }  // namespace
 }  // namespace muon
 
@@ -44,6 +55,9 @@ int muon_grad_norm(const void* const* grads, const int64_t* numels, const int* d
     clear_error();
     const int rc = validate_grad_norm(grads, numels, dtypes, n, max_norm, scale, record, workspace);
     if (rc) return rc;
+    GradSmallArgs small;
+    if (grad_small(grads, nullptr, numels, dtypes, nullptr, n, &small))
+      return enqueue_small(small, false, max_norm, scale, record, stream);
     // without a limit the norm is wanted for itself
     std::vector<NormArgs> norm = norm_launches(grads, numels, dtypes, n, std::isinf(max_norm) ? 0 : NORM_KEEP_BYTES);
     std::lock_guard<std::mutex> lock(api_mutex());
@@ -58,6 +72,9 @@ int muon_grad_clip(const void* const* grads, void* const* outs, const int64_t* n
     clear_error();
     int rc = validate_grad_clip(grads, outs, numels, dtypes, out_dtypes, n, max_norm, scale, record, workspace);
     if (rc) return rc;
+    GradSmallArgs small;
+    if (grad_small(grads, outs, numels, dtypes, out_dtypes, n, &small))
+      return enqueue_small(small, true, max_norm, scale, record, stream);
     std::vector<ClipArgs> clip = clip_launches(grads, outs, numels, dtypes, out_dtypes, n);
     // in place the gradients are usually not read again
     bool in_place = true;

@@ -187,6 +187,24 @@ int validate_step_record(float* const* params, float* const* moms, uint16_t* con
   return check_spans(s);
 }
 
+bool grad_small(const void* const* grads, void* const* outs, const int64_t* numels, const int* types,
+                const int* out_types, int n, GradSmallArgs* out) {
+  GradSmallArgs a{};
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] == 0) continue;
+    const Cut c = cut_of(numels[i], norm_chunk(types[i]));
+    if (a.items + c.items > NORM_SMALL_ITEMS) return false;  // then there are no more tensors than items either
+    a.tail[a.n] = c.last << 4 | (uint32_t)(outs ? out_types[i] : 0) << 2 | (uint32_t)types[i];
+    a.in[a.n] = grads[i];
+    a.out[a.n] = outs ? outs[i] : nullptr;
+    a.items += (int32_t)c.items;
+    a.start[++a.n] = a.items;
+  }
+  fill_unused(a);
+  *out = a;
+  return true;
+}
+
 std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* numels, const int* types, int n,
                                     int64_t keep_bytes) {
   std::vector<NormArgs> out(1, NormArgs{});
@@ -214,7 +232,6 @@ std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* num
   }
   int32_t most = 1;
   for (const NormArgs& a : out) most = std::max(most, a.items);
-  if (out.size() == 1 && most <= NORM_SMALL_ITEMS) most = 1;
   for (NormArgs& a : out) a.blocks = std::min(most, (int32_t)NORM_MAX_BLOCKS);
   return out;
 }

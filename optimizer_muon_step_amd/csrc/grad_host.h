@@ -30,6 +30,10 @@ int validate_step_record(float* const* params, float* const* moms, uint16_t* con
 // ---- launch tables: pointers, items and flags; scalars are the caller's ----
 // Tensors without elements take no part.  There is always at least one norm
 // launch (it writes the record), all of one grid; the others may have none.
+// Whether a norm or clip of these tensors is one small launch (outs and
+// out_types null for a norm).
+bool grad_small(const void* const* grads, void* const* outs, const int64_t* numels, const int* types,
+                const int* out_types, int n, GradSmallArgs* out);
 // keep_bytes: how much of the list's end the norm reads so as to stay cached.
 std::vector<NormArgs> norm_launches(const void* const* grads, const int64_t* numels, const int* types, int n,
                                     int64_t keep_bytes);

@@ -40,8 +40,8 @@ constexpr int NORM_MAX_BLOCKS = 1024;    // partial sums in the workspace
 // and 196 us, of 124 M 686 and 642 us; norm and clip of 124 M bf16 elements
 // into fp32 170 and 155 us.
 constexpr int64_t NORM_KEEP_BYTES = (int64_t)256 << 20;
-// A call of at most NORM_SMALL_ITEMS items is one block, a wave to an item,
-// and needs no arrivals.
+// A norm or clip of at most NORM_SMALL_ITEMS items (256 KB) is one launch of
+// one block, a wave to an item.
 constexpr int NORM_SMALL_ITEMS = 16;
 constexpr int NORM_SMALL_THREADS = 1024;
 constexpr int NORM_GROUP = 32;           // blocks that count on one counter
@@ -62,8 +62,7 @@ struct NormWorkspace {
 };
 
 constexpr int NORM_TENSORS = (KERNARG_BYTES - 64) / 16;
-template <int TENSORS>
-struct NormTable {
+struct NormArgs {
   NormWorkspace* ws;
   float* record;        // {norm, factor}
   float max_norm, scale;
@@ -71,12 +70,10 @@ struct NormTable {
   int32_t blocks;       // grid of every launch of the call
   int32_t first, last;  // first / last launch of the call
   int32_t keep_from;    // items from here on are read so as to stay in the memory-side cache
-  int32_t start[TENSORS + 1];
-  uint32_t tail[TENSORS];  // elements of the last chunk << 2 | type
-  const void* p[TENSORS];
+  int32_t start[NORM_TENSORS + 1];
+  uint32_t tail[NORM_TENSORS];  // elements of the last chunk << 2 | type
+  const void* p[NORM_TENSORS];
 };
-typedef NormTable<NORM_TENSORS> NormArgs;
-typedef NormTable<NORM_SMALL_ITEMS> NormSmallArgs;
 static_assert(sizeof(NormArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // ---- clipping ----
@@ -102,6 +99,17 @@ struct ClipArgs {
   void* out[CLIP_TENSORS];
 };
 static_assert(sizeof(ClipArgs) <= KERNARG_BYTES, "kernel arguments");
+
+// ---- norm, or norm and clip, of a small call ----
+struct GradSmallArgs {
+  float* record;
+  float max_norm, scale;
+  int32_t n, items;
+  int32_t start[NORM_SMALL_ITEMS + 1];
+  uint32_t tail[NORM_SMALL_ITEMS];  // elements of the last chunk << 4 | output type << 2 | type
+  const void* in[NORM_SMALL_ITEMS];
+  void* out[NORM_SMALL_ITEMS];  // of a clip
+};
 
 // ---- AdamW on clipped gradients ----
 // Elements per work item: long chunks, in per-XCD runs of ADAMC_LONG_RUN, for

@@ -37,6 +37,7 @@ hipError_t launch_adamw(const AdamDesc* d, const EwItem* items, int n_items, con
 
 // Gradient norm, clipping, and AdamW on clipped gradients: one launch each.
 hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_grad_small(const GradSmallArgs& a, bool clip, hipStream_t s);
 hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t s);
 hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s);
 

@@ -142,6 +142,30 @@ static void check_clip(const List& l) {
   for (int i = 0; i < l.n(); ++i) CHECK(got[l.out[i]] == l.numel[i]);
 }
 
+static void check_small(const List& l) {
+  GradSmallArgs a, b;
+  int64_t items = 0;
+  for (int i = 0; i < l.n(); ++i) items += (l.numel[i] + norm_chunk(l.type[i]) - 1) / norm_chunk(l.type[i]);
+  const bool small = grad_small(l.g.data(), l.out.data(), l.numel.data(), l.type.data(), l.out_type.data(), l.n(), &a);
+  CHECK(small == (items <= NORM_SMALL_ITEMS));
+  CHECK(small == grad_small(l.g.data(), nullptr, l.numel.data(), l.type.data(), nullptr, l.n(), &b));
+  if (!small) return;
+  CHECK(a.n <= NORM_SMALL_ITEMS && a.items == items && b.items == items && b.n == a.n);
+  std::map<int, std::vector<std::pair<int64_t, int>>> seen;
+  for (int wave = 0; wave < NORM_SMALL_ITEMS; ++wave)
+    if (wave < a.items)
+      walk(a.start, NORM_SMALL_ITEMS + 1, a.n, wave, NORM_SMALL_ITEMS, [&](int t) { return (int)(a.tail[t] >> 4); },
+           [&](int t) { return norm_chunk(a.tail[t] & 3); }, &seen);
+  std::map<const void*, int64_t> got;
+  for (auto& s : seen) got[a.out[s.first]] += covered(s.second);
+  for (int i = 0; i < l.n(); ++i) {
+    CHECK(got[l.out[i]] == l.numel[i]);
+    for (int t = 0; t < a.n; ++t)
+      if (a.out[t] == l.out[i])
+        CHECK(a.in[t] == l.g[i] && (int)(a.tail[t] & 3) == l.type[i] && (int)(a.tail[t] >> 2 & 3) == l.out_type[i]);
+  }
+}
+
 static void check_adamw(const List& l, bool with_wd) {
   int64_t total = 0;
   for (int64_t m : l.numel) total += m;
@@ -255,16 +279,23 @@ static void check_refusals() {
 }
 
 int main() {
-  for (int n : {0, 1, 2, 5, 99, 100, 101, 167, 168, 169, 251, 252, 253, 600}) {
+  for (int n : {0, 1, 2, 3, 4, 5, 6, 7, 8, 99, 100, 101, 167, 168, 169, 251, 252, 253, 600}) {
     for (int decays : {1, 4, 5, 9}) {
       const List l = make_list(n, decays);
       if (decays == 1) {
         for (int64_t keep : {(int64_t)0, (int64_t)1 << 20, NORM_KEEP_BYTES}) check_norm(l, keep);
         check_clip(l);
+        check_small(l);
       }
       check_adamw(l, true);
       check_adamw(l, false);
     }
+  }
+  // as many items as the small call takes, and one more
+  for (int n : {15, 16, 17}) {
+    List l = make_list(n, 1);
+    for (int i = 0; i < n; ++i) l.numel[i] = i % 2 ? 1 : norm_chunk(l.type[i]);
+    check_small(l);
   }
   // a call long enough for the long chunks
   {

@@ -209,6 +209,37 @@ def test_clip_in_place(kind):
         assert np.array_equal(_values(b).view(np.uint32), want.view(np.uint32))
 
 
+@pytest.mark.parametrize("kind_in", KINDS)
+@pytest.mark.parametrize("kind_out", KINDS + ("in place",))
+@pytest.mark.parametrize("offset", [0, 1, 5])
+def test_small_clips(kind_in, kind_out, offset):
+    """Calls of one launch: a tensor of each size alone, then lists of up to
+    16 chunks, below and above the limit; nothing outside an out is written."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    rng = np.random.default_rng(70)
+    chunk = 4096 if kind_in == "fp32" else 8192
+    lists = [[n] for n in EDGES] + [[], [0, 3], [chunk] * 16, [chunk * 15 + 1], [1] * 16, [chunk - 1, 2 * chunk + 3, 1, 0, 700]]
+    for sizes in lists:
+        for limit in (1e9, 0.25):
+            bufs = _make(rng, [n + offset + 4 for n in sizes], [kind_in])
+            g = [b[offset:-4] for b in bufs]
+            before = [b.clone() for b in bufs]
+            if kind_out == "in place":
+                obufs, outs, kind = bufs, None, kind_in
+            else:
+                kind = kind_out
+                obufs = [torch.full((n + offset + 4,), -7.0, dtype=_dtype(kind), device="cuda") for n in sizes]
+                outs = [b[offset:-4] for b in obufs]
+            record = mu.muon_grad_clip(g, limit, outs=outs)
+            got = _check_record(record, [b[offset:-4] for b in before], limit)
+            assert torch.equal(_bits(record), _bits(mu.muon_grad_norm([b[offset:-4] for b in before], limit)))
+            for b, k in zip(obufs, before):
+                want = _values(k) if outs is None else np.full(b.numel(), -7.0, np.float32)
+                want[offset:-4] = go.rounded(go.clipped(_values(k)[offset:-4], np.float32(got[1])), kind)
+                assert np.array_equal(_values(b).view(np.uint32), want.view(np.uint32)), (sizes, limit)
+
+
 def test_clip_scale_alone_and_many_tensors():
     """No limit: only the scale; more tensors than one launch's table holds."""
     import optimizer_muon_step_amd as mu
@@ -312,6 +343,26 @@ def test_captured_norm_and_clip_without_an_earlier_call():
             torch.cuda.synchronize()
             assert torch.equal(_bits(record), _bits(eager)), rep
             assert all(torch.equal(a, b) for a, b in zip(outs, eager_outs)), rep
+
+
+def test_captured_norm_clears_its_workspace():
+    """The graph's memory is not clear: the graph clears the norm's part of it
+    on every replay."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    g = _make(np.random.default_rng(71), [300_001, 5, 40_000], KINDS)
+    want = mu.muon_grad_norm(g, 1.0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        junk = torch.full((8192,), 7.0, dtype=torch.float64, device="cuda")
+        del junk  # what is allocated next gets its memory
+        record = mu.muon_grad_norm(g, 1.0)
+    for _ in range(3):
+        record.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(record), _bits(want))
 
 
 def test_timing_families():
