@@ -44,6 +44,14 @@ def _check(rc: int) -> None:
         raise MuonError(rc, muon_last_error())
 
 
+def _current_device():
+    """torch's current GPU, or -1 where there is none (then no tensor is on it)."""
+    import torch
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -1
+
+
 def _stream_handle(stream):
     if stream is None:
         import torch
@@ -224,19 +232,6 @@ def _as_list(ts):
     return ts if isinstance(ts, (list, tuple)) else list(ts)
 
 
-def _check_device(what, dev):
-    import torch
-    if dev >= 0 and dev != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensors on GPU {dev}, the current one is {torch.cuda.current_device()}")
-
-
-def _flat_list(ts, what, any_type, dense):
-    """(addresses, element counts, type codes) of a list of tensors taken flat, as C arrays."""
-    ptrs, numels, types, dev = _lib.load_tensor_args().flat(ts, what, any_type, dense)
-    _check_device(what, dev)
-    return ptrs, numels, types
-
-
 def _record_ptr(record):
     import torch
     if (not isinstance(record, torch.Tensor) or record.dtype != torch.float32 or record.numel() != 2
@@ -245,19 +240,9 @@ def _record_ptr(record):
     return record.data_ptr()
 
 
-class _NoStream:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return None
-
-
 def _on_stream(stream):
     """A context in which `stream` is torch's current one, so that what a call
     allocates belongs to the stream that uses it."""
-    if stream is None:
-        return _NoStream()
     import torch
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
@@ -269,22 +254,19 @@ def _on_stream(stream):
 _norm_workspaces = {}
 
 
-def _norm_buffers(record):
-    """(record, workspace, stream handle) of a norm on torch's current stream.
-    A captured call takes a workspace of its own from the graph's memory,
-    cleared by the graph, so that graphs share none either."""
+def _norm_workspace(dev, handle):
+    """The workspace of a norm on torch's current stream.  A captured call
+    takes one of its own from the graph's memory, cleared by the graph, so
+    that graphs share none either."""
     import torch
-    handle, dev = _stream_handle(None), torch.cuda.current_device()
-    if record is None:
-        record = torch.empty(2, dtype=torch.float32, device=dev)
-    else:
-        _record_ptr(record)
+    if dev < 0:
+        return torch.empty(0)
     if torch.cuda.is_current_stream_capturing():
-        return record, torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev), handle
+        return torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
     ws = _norm_workspaces.get((dev, handle))
     if ws is None:
         ws = _norm_workspaces[dev, handle] = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
-    return record, ws, handle
+    return ws
 
 
 def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
@@ -298,14 +280,20 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
     n = len(params)
     if not (len(grads) == len(exp_avg) == len(exp_avg_sq) == n):
         raise ValueError("params, grads, exp_avg and exp_avg_sq must have the same length")
-    if hasattr(weight_decay, "__len__"):
-        if len(weight_decay) != n:
-            raise ValueError("weight_decay: expected one value or one per tensor")
-        wds = _lib.float_array(weight_decay)
-    else:
-        wds = _lib.float_array([weight_decay] * n)
     if clip is not None or _any_16_bit(grads):
-        return _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip)
+        dev = _current_device()
+        wd = weight_decay if not hasattr(weight_decay, "__len__") else _as_list(weight_decay)
+        b1, b2 = betas
+        _check(_lib.load_tensor_calls().adamw_clip(
+            _as_list(params), _as_list(grads), _as_list(exp_avg), _as_list(exp_avg_sq), wd, float(lr), float(b1),
+            float(b2), float(eps), int(step), clip, dev, _stream_handle(stream) if dev >= 0 else 0))
+        return
+    if hasattr(weight_decay, "__len__"):
+        wds = [float(w) for w in weight_decay]
+        if len(wds) != n:
+            raise ValueError("weight_decay: expected one value or one per tensor")
+    else:
+        wds = [float(weight_decay)] * n
     ptrs = ([], [], [], [])
     numels = []
     for i in range(n):
@@ -318,28 +306,9 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
         numels.append(params[i].numel())
     b1, b2 = betas
     rc = _lib.load().muon_adamw_step(*(_lib.ptr_array(p) for p in ptrs), _lib.int64_array(numels),
-                                     wds, n, float(lr), float(b1), float(b2), float(eps),
+                                     _lib.float_array(wds), n, float(lr), float(b1), float(b2), float(eps),
                                      int(step), ctypes.c_void_p(_stream_handle(stream)))
     _check(rc)
-
-
-def _adamw_step_clip(params, grads, exp_avg, exp_avg_sq, lr, betas, eps, wds, step, stream, clip):
-    n = len(params)
-    flat = _lib.load_tensor_args().flat
-    p, numels, _, dev = flat(params, "params", False, False)
-    g, g_numels, types, g_dev = flat(grads, "grads", True, False)
-    u, u_numels, _, u_dev = flat(exp_avg, "exp_avg", False, False)
-    v, v_numels, _, v_dev = flat(exp_avg_sq, "exp_avg_sq", False, False)
-    if not dev == g_dev == u_dev == v_dev:
-        raise ValueError(f"params, grads, exp_avg and exp_avg_sq on GPUs {dev}, {g_dev}, {u_dev} and {v_dev}")
-    _check_device("params", dev)
-    if not numels == g_numels == u_numels == v_numels:
-        i = next(i for i in range(n) if len({ts[i].numel() for ts in (params, grads, exp_avg, exp_avg_sq)}) != 1)
-        raise ValueError(f"tensor {i}: element counts differ")
-    record = None if clip is None else _record_ptr(clip)
-    b1, b2 = betas
-    _check(_lib.load().muon_adamw_step_clip(p, g, types, u, v, numels, wds, n, float(lr), float(b1), float(b2),
-                                            float(eps), int(step), record, _stream_handle(stream)))
 
 
 def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=None):
@@ -352,12 +321,14 @@ def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=
     as `clip` to muon_step and muon_adamw_step, which then take the gradients
     clipped without a pass that writes them back.  `record` is a tensor of 2
     to fill instead of a new one."""
-    grads = _as_list(grads)
-    ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
-    with _on_stream(stream):
-        record, ws, st = _norm_buffers(record)
-        _check(_lib.load().muon_grad_norm(ptrs, numels, types, len(grads), float(max_norm), float(scale),
-                                          record.data_ptr(), ws.data_ptr(), st))
+    if stream is not None:
+        with _on_stream(stream):
+            return muon_grad_norm(grads, max_norm, scale, record)
+    dev = _current_device()
+    handle = _stream_handle(None) if dev >= 0 else 0
+    ws = _norm_workspace(dev, handle)
+    rc, record = _lib.load_tensor_calls().grad_norm(_as_list(grads), max_norm, scale, record, ws.data_ptr(), dev, handle)
+    _check(rc)
     return record
 
 
@@ -367,22 +338,15 @@ def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=No
     same shapes and memory order and of any of the three types (16-bit
     gradients into float32 ones, say).  Returns the record {norm, factor};
     the norm is the one before clipping."""
-    grads = _as_list(grads)
-    ptrs, numels, types = _flat_list(grads, "grads", any_type=True, dense=True)
-    if outs is None:
-        out_ptrs, out_types = ptrs, types
-    else:
-        outs = _as_list(outs)
-        if len(outs) != len(grads):
-            raise ValueError("grads and outs must have the same length")
-        out_ptrs, _, out_types = _flat_list(outs, "outs", any_type=True, dense=True)
-        i = _lib.load_tensor_args().first_unlike(grads, outs)
-        if i >= 0:
-            raise ValueError(f"outs[{i}]: shape or memory order differs from grads[{i}]")
-    with _on_stream(stream):
-        record, ws, st = _norm_buffers(record)
-        _check(_lib.load().muon_grad_clip(ptrs, out_ptrs, numels, types, out_types, len(grads), float(max_norm),
-                                          float(scale), record.data_ptr(), ws.data_ptr(), st))
+    if stream is not None:
+        with _on_stream(stream):
+            return muon_grad_clip(grads, max_norm, scale, outs, record)
+    dev = _current_device()
+    handle = _stream_handle(None) if dev >= 0 else 0
+    ws = _norm_workspace(dev, handle)
+    rc, record = _lib.load_tensor_calls().grad_clip(_as_list(grads), None if outs is None else _as_list(outs), max_norm,
+                                                    scale, record, ws.data_ptr(), dev, handle)
+    _check(rc)
     return record
 
 

@@ -36,7 +36,7 @@ SIGNATURES = {
     "muon_adamw_untie": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _P]),
     "muon_grad_norm": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
     "muon_grad_clip": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
-    "muon_adamw_step_clip": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _FLOAT3, ctypes.c_int, ctypes.c_float,
+    "muon_adamw_step_clip": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_float,
                                             ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_int64, _P, _P]),
     "muon_step_clip": (ctypes.c_int, [_PP, _PP, _PP, _SHAPES, ctypes.c_int, ctypes.c_float, ctypes.c_float,
                                       ctypes.c_int, _FLOAT3, _PP, _P, _P]),
@@ -51,7 +51,7 @@ SIGNATURES = {
 }
 
 _lib = None
-_tensor_args = None
+_tensor_calls = None
 
 
 def load() -> ctypes.CDLL:
@@ -71,19 +71,20 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-def load_tensor_args():
-    """The compiled reader of tensor lists; raises if it has not been built."""
-    global _tensor_args
-    if _tensor_args is None:
+def load_tensor_calls():
+    """The library's calls on tensor lists; raises if they have not been built."""
+    global _tensor_calls
+    if _tensor_calls is None:
+        load()  # the library they call
         import torch  # noqa: F401  (its libraries, which the module links against)
         try:
-            from . import _tensor_args as module
+            from . import _tensor_calls as module
         except ImportError as e:
             raise RuntimeError(
-                "_tensor_args.so is missing: build it with `python -m optimizer_muon_step_amd.build` "
+                "_tensor_calls.so is missing: build it with `python -m optimizer_muon_step_amd.build` "
                 f"(or __graft_entry__.build()); there is no fallback implementation ({e})") from e
-        _tensor_args = module
-    return _tensor_args
+        _tensor_calls = module
+    return _tensor_calls
 
 
 def ptr_array(ptrs):

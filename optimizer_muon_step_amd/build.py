@@ -1,6 +1,6 @@
 """Build libmuon.so (the gfx950 HIP kernels and the C ABI) in place with
 hipcc, the plain C caller muon_c_example linked against it, and the binding's
-reader of tensor lists."""
+calls on tensor lists."""
 from __future__ import annotations
 
 import hashlib
@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmuon.so")
-TENSOR_ARGS = os.path.join(HERE, "_tensor_args.so")
+TENSOR_CALLS = os.path.join(HERE, "_tensor_calls.so")
 C_EXAMPLE = os.path.join(HERE, "muon_c_example")
 SOURCES = ["muon_api.hip", "muon_noalloc.hip", "plan_host.cpp", "kernels_tables.hip", "kernels_momentum.hip", "kernels_elementwise.hip",
            "kernels_ns.hip", "kernels_ns_gram.hip", "kernels_ns_fused.hip", "kernels_adamw.hip", "grad_api.hip",
@@ -111,31 +111,33 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB,
     os.replace(tmp, out)
     if out == LIB:
         build_c_example(verbose)
-        build_tensor_args(verbose)
+        build_tensor_calls(verbose)
     return out
 
 
-def build_tensor_args(verbose: bool = False) -> str:
-    """Compile csrc/tensor_args.cpp with the host C++ compiler against torch."""
+def build_tensor_calls(verbose: bool = False) -> str:
+    """Compile csrc/tensor_calls.cpp with the host C++ compiler, against torch
+    and libmuon.so."""
     import torch
     cxx = shutil.which("g++") or shutil.which("c++")
     if not cxx:
         raise RuntimeError("no host C++ compiler")
     at = os.path.dirname(torch.__file__)
-    tmp = TENSOR_ARGS + ".tmp"
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    tmp = TENSOR_CALLS + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-isystem", os.path.join(at, "include"), "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_args.cpp"),
-           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp]
+           "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_calls.cpp"),
+           "-L", HERE, "-lmuon", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"{cxx} failed with exit code {res.returncode}")
-    os.replace(tmp, TENSOR_ARGS)
-    return TENSOR_ARGS
+    os.replace(tmp, TENSOR_CALLS)
+    return TENSOR_CALLS
 
 
 def build_c_example(verbose: bool = False) -> str:

@@ -26,6 +26,8 @@ std::string name_of(const Span& s) {
   return s.tensor < 0 ? std::string(s.what) : std::string(s.what) + "[" + std::to_string(s.tensor) + "]";
 }
 
+bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
 // No written array may overlap another one; read arrays may share memory.
 int check_spans(std::vector<Span>& v) {
   std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
@@ -102,17 +104,19 @@ int validate_grad_norm(const void* const* grads, const int64_t* numels, const in
   if (n > 0 && (!grads || !numels || !types))
     return fail(MUON_EINVAL, "grads, numels and dtypes arrays must not be NULL");
   if ((rc = check_clip_scalars(max_norm, scale, record, workspace))) return rc;
-  std::vector<Span> v;
-  v.reserve((size_t)n + 2);
-  v.push_back(span_of(record, MUON_CLIP_RECORD_FLOATS * sizeof(float), true, -1, "record"));
-  v.push_back(span_of(workspace, MUON_GRAD_WORKSPACE_BYTES, true, -1, "workspace"));
+  // only these two are written: no need to put every gradient in order
+  const Span written[2] = {span_of(record, MUON_CLIP_RECORD_FLOATS * sizeof(float), true, -1, "record"),
+                           span_of(workspace, MUON_GRAD_WORKSPACE_BYTES, true, -1, "workspace")};
+  if (overlap(written[0], written[1])) return fail(MUON_EINVAL, "record overlaps workspace");
   for (int i = 0; i < n; ++i) {
     if ((rc = check_numel(numels, i)) || (rc = check_type(types, i, "dtypes"))) return rc;
     if (numels[i] == 0) continue;
     if ((rc = check_ptr(grads[i], types[i], i, "grads"))) return rc;
-    v.push_back(span_of(grads[i], (size_t)numels[i] * grad_type_bytes(types[i]), false, i, "grads"));
+    const Span g = span_of(grads[i], (size_t)numels[i] * grad_type_bytes(types[i]), false, i, "grads");
+    for (const Span& w : written)
+      if (overlap(w, g)) return fail(MUON_EINVAL, "%s overlaps %s", w.what, name_of(g).c_str());
   }
-  return check_spans(v);
+  return MUON_OK;
 }
 
 int validate_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* types,
@@ -265,9 +269,21 @@ std::vector<AdamClipArgs> adamw_clip_launches(float* const* params, const void* 
   int64_t total = 0;
   for (int i = 0; i < n; ++i) total += numels[i];
   const int chunk = total >= ADAMC_LONG_MIN ? ADAMC_LONG_CHUNK : ADAMC_CHUNK;
-  int decays = 0;  // distinct ones of the last launch so far
+  // A launch holds ADAMC_DECAYS distinct decays: with more of them the tensors
+  // are taken decay by decay (their order changes no result).
+  std::vector<int> order;
+  std::vector<float> seen;
   for (int i = 0; i < n; ++i) {
     if (numels[i] == 0) continue;
+    order.push_back(i);
+    const float lambda = wd ? wd[i] : 0.0f;
+    if (seen.size() <= (size_t)ADAMC_DECAYS && std::find(seen.begin(), seen.end(), lambda) == seen.end())
+      seen.push_back(lambda);
+  }
+  if (seen.size() > (size_t)ADAMC_DECAYS)
+    std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return wd[x] < wd[y]; });
+  int decays = 0;  // distinct ones of the last launch so far
+  for (int i : order) {
     const Cut c = cut_of(numels[i], chunk);
     const float lambda = wd ? wd[i] : 0.0f;
     int k = 0;

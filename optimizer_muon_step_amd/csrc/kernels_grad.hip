@@ -153,7 +153,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_norm_kernel(const NormArgs 
   s = block_sum_f64<kWavesG>(s, red);
   NormWorkspace* ws = a.ws;
   if (threadIdx.x == 0) {
-    if (!a.first) s += ws->part[blockIdx.x];
+    if (!a.first) s += __hip_atomic_load(&ws->part[blockIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(&ws->part[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     is_last = a.last && last_arrival(ws, a.blocks);
   }

@@ -304,13 +304,16 @@ int main() {
     check_adamw(l, true);
     check_norm(l, NORM_KEEP_BYTES);
   }
-  // five decays in turn need a launch per four; grouped, as many as fit one
+  // two decays in one launch; nine need three launches, in whatever order they come
   {
     List l = make_list(60, 5);
     for (int i = 0; i < 60; ++i) l.numel[i] = 64;
     for (int i = 0; i < 60; ++i) l.wd[i] = i < 30 ? 0.0f : 0.1f;
     CHECK(adamw_clip_launches(l.p.data(), l.g.data(), l.type.data(), l.u.data(), l.v.data(), l.numel.data(),
                               l.wd.data(), 60).size() == 1);
+    for (int i = 0; i < 60; ++i) l.wd[i] = 0.01f * (float)(i % 9);  // in turn: taken decay by decay
+    CHECK(adamw_clip_launches(l.p.data(), l.g.data(), l.type.data(), l.u.data(), l.v.data(), l.numel.data(),
+                              l.wd.data(), 60).size() == 3);
   }
   // a list whose items pass the grid limit is cut, and offsets pass 32 bits
   {

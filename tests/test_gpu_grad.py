@@ -314,6 +314,32 @@ def test_two_streams_at_once():
     assert torch.equal(_bits(record), _bits(want[0]))
 
 
+def test_two_threads_on_one_stream():
+    """Both threads' calls take the stream's one workspace, and several
+    launches each: a call's launches stay together."""
+    import threading
+
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    rng = np.random.default_rng(72)
+    lists = [_make(rng, [1000 + k for k in range(600)], ["fp32"]), _make(rng, [700 + 3 * k for k in range(550)], KINDS)]
+    want = [mu.muon_grad_norm(g, 1.0) for g in lists]
+    got = [[], []]
+
+    def work(k):
+        for _ in range(50):
+            got[k].append(mu.muon_grad_norm(lists[k], 1.0))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert len(got[k]) == 50 and all(torch.equal(_bits(r), _bits(want[k])) for r in got[k])
+
+
 def test_captured_norm_and_clip_without_an_earlier_call():
     """Captured at once, replayed with new gradients and eager work between;
     two graphs replayed in turn."""

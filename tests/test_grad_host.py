@@ -86,8 +86,18 @@ def test_binding_refuses():
             call()
     with pytest.raises(ValueError, match="expected a tensor"):
         mu.muon_grad_norm([None])
-    with pytest.raises(TypeError, match="list of tensors"):
-        _lib.load_tensor_args().flat(3, "grads", True, True)
+    with pytest.raises(ValueError, match="list of tensors"):
+        _lib.load_tensor_calls().grad_norm(3, 1.0, 1.0, None, 0, -1, 0)
+    with pytest.raises(TypeError):
+        mu.muon_grad_norm([], max_norm="1")
+    with pytest.raises(ValueError, match="weight_decay"):
+        mu.muon_adamw_step([], [], [], [], 1e-3, weight_decay=[0.1], clip=0)
+    with pytest.raises(ValueError, match="weight_decay"):
+        mu.muon_adamw_step([], [], [], [], 1e-3, weight_decay="x", clip=0)
+    with pytest.raises(ValueError, match="record"):
+        mu.muon_adamw_step([], [], [], [], 1e-3, clip=0)
+    with pytest.raises(ValueError, match="record"):
+        mu.muon_grad_norm([], record=torch.zeros(2))
     with pytest.raises(ValueError, match="bfloat16 or float16, not Double"):
         mu.muon_grad_norm([cpu.double()])
     with pytest.raises(ValueError, match="not Int"):
@@ -111,18 +121,6 @@ def test_dense_layouts():
             mu.muon_grad_norm([g])
     with pytest.raises(ValueError, match=r"params\[0\]: expected a contiguous tensor"):
         mu.muon_adamw_step([t.permute(2, 0, 1)], [t.half()], [t], [t], 1e-3)
-
-
-def test_lists_alike():
-    import torch
-
-    from optimizer_muon_step_amd import _lib as lib
-    unlike = lib.load_tensor_args().first_unlike
-    t = torch.zeros(4, 5)
-    assert unlike([t, t], (t, t.clone())) == -1 and unlike([], []) == -1
-    assert unlike([t, t], [t, t.t()]) == 1 and unlike([t.t()], [t.t().clone()]) == -1
-    assert unlike([t], [t.view(5, 4)]) == 0 and unlike([t], [None]) == 0
-    assert unlike([torch.zeros(1, 5)], [torch.zeros(5, 1).t()]) == -1
 
 
 def test_oracle_closed_forms():
