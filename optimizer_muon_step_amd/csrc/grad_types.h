@@ -22,9 +22,8 @@ constexpr int grad_type_bytes(int t) { return t == GRAD_FP32 ? 4 : 2; }
 // Work items of a launch are chunks of its tensors: tensor t owns items
 // start[t] .. start[t + 1] - 1, all of the full chunk length except the last,
 // whose elements are counted in tail[t] (shifted past the type bits); start
-// holds START_UNUSED behind start[n].  A grid
-// holds fewer than 2^32 threads, so a launch of one block per item takes
-// fewer than 2^24 items.
+// holds START_UNUSED behind start[n].  A grid holds fewer than 2^32 threads,
+// so a launch of one block per item takes fewer than 2^24 items.
 constexpr int32_t START_UNUSED = INT32_MAX;
 constexpr int64_t MAX_LAUNCH_ITEMS = (1 << 24) - 1;
 constexpr int64_t GRAD_MAX_NUMEL = (int64_t)1 << 35;
@@ -36,15 +35,17 @@ constexpr int NORM_MAX_BLOCKS = 1024;    // partial sums in the workspace
 // NORM_KEEP_BYTES of a call (the memory-side cache's size) are read with plain
 // loads, which leave them in that cache, and what is before them with
 // non-temporal ones, which are faster.  Measured with 0 and with 256 MiB
-// kept: norm of 495 MB 77 and 84 us; norm and AdamW of 39.5 M elements 216
-// and 196 us, of 124 M 686 and 642 us; norm and clip of 124 M bf16 elements
-// into fp32 170 and 155 us.
+// kept: norm of 498 MB 75 and 79 us; norm and AdamW of 39.5 M elements 211
+// and 191 us, of 124 M 676 and 639 us; norm and clip of 124 M bf16 elements
+// into fp32 163 and 147 us.
 constexpr int64_t NORM_KEEP_BYTES = (int64_t)256 << 20;
 // A norm or clip of at most NORM_SMALL_ITEMS items (256 KB) is one launch of
-// one block, a wave to an item.
+// one block, a wave to an item: a norm takes 6.8 us a call against 7.8 by the
+// other kernels, a clip 7.0 against 12.4, of 2 items, and 6.7 and 7.8, 7.7
+// and 12.3 of 16.
 constexpr int NORM_SMALL_ITEMS = 16;
 constexpr int NORM_SMALL_THREADS = 1024;
-constexpr int NORM_GROUP = 32;           // blocks that count on one counter
+constexpr int NORM_GROUP = 32;  // blocks that count on one counter
 constexpr int NORM_MAX_GROUPS = NORM_MAX_BLOCKS / NORM_GROUP;
 constexpr int norm_chunk(int type) { return NORM_CHUNK_BYTES / grad_type_bytes(type); }
 
@@ -77,13 +78,14 @@ struct NormArgs {
 static_assert(sizeof(NormArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // ---- clipping ----
-// Out of place one block per item, in per-XCD runs of CLIP_RUN items (clip of
-// 1.56 G bf16 elements 1490 -> 1431 us with its norm, 124 M bf16 into fp32
-// 155 -> 150; fp32 sets alike).  In place a factor of 1, the usual one, ends every block at
+// Out of place one block per item, in per-XCD runs of CLIP_RUN items; without
+// the runs and with them, norm included: 1.56 G bf16 elements 1486 and 1460
+// us, 124 M bf16 into fp32 152 and 148, 124 M fp32 227 and 226, 39.5 M fp32
+// 72 and 74.  In place a factor of 1, the usual one, ends every block at
 // once, and dispatching them is then all the time there is (1.3 ns each): at
-// most CLIP_IN_PLACE_BLOCKS take the items in turn (1.56 G bf16 elements
-// below the limit 540 -> 468 us with the norm, clipped 1451 -> 1590; 124 M
-// fp32 elements 91 -> 89 and 231 -> 220).
+// most CLIP_IN_PLACE_BLOCKS take the items in turn.  With a block per item
+// and with that many: 1.56 G bf16 elements below the limit 541 and 468 us,
+// clipped 1494 and 1603; 124 M fp32 elements 83 and 80, 237 and 236.
 constexpr int CLIP_CHUNK = 4096;  // elements
 constexpr int CLIP_RUN = 64;
 constexpr int CLIP_IN_PLACE_BLOCKS = 16384;
@@ -114,13 +116,13 @@ struct GradSmallArgs {
 // ---- AdamW on clipped gradients ----
 // Elements per work item: long chunks, in per-XCD runs of ADAMC_LONG_RUN, for
 // calls of at least ADAMC_LONG_MIN elements.  Measured with short and with
-// long chunks, norm included: 1.56 G elements with bf16 gradients 7.62 and
-// 7.45 ms (7.22 in runs), 124 M fp32 642 and 636 us (runs 647), 39.5 M fp32 196 and 201 us
-// (fewer, larger blocks end less evenly).
+// long chunks, norm included: 39.5 M fp32 elements 193 and 200 us (fewer,
+// larger blocks end less evenly), 124 M fp32 642 and 625 us, 1.56 G with bf16
+// gradients 7.5 and 7.2 ms (7.5 without the runs).
 constexpr int ADAMC_CHUNK = 4096, ADAMC_LONG_CHUNK = 8192;
 constexpr int ADAMC_LONG_RUN = 16;
-constexpr int64_t ADAMC_LONG_MIN = (int64_t)1 << 27;
-constexpr int ADAMC_DECAYS = 4;    // distinct weight decays of a launch
+constexpr int64_t ADAMC_LONG_MIN = (int64_t)1 << 26;
+constexpr int ADAMC_DECAYS = 4;  // distinct weight decays of a launch
 constexpr int ADAMC_TENSORS = (KERNARG_BYTES - 80) / 40;
 struct AdamClipArgs {
   const float* record;  // {norm, factor}, or null: factor 1

@@ -166,6 +166,10 @@ __device__ __forceinline__ void adamw_clip_chunk(const AdamClipArgs& a, int t, i
 
 }  // namespace
 
+// Bound by HBM: 39.5 M elements with fp32 gradients, 1106 MB, in 162 us (6.8
+// TB/s, the gradients from the memory-side cache, where the norm left them);
+// 1.56 G with bf16 gradients, 40.5 GB, in 6.8 ms (5.9 TB/s).
+//
 // The AdamW step on clipped gradients: the factor is read from the record on
 // the device.  A norm that is not finite leaves everything as it was.
 template <int CHUNK>

@@ -290,6 +290,31 @@ def test_clip_keeps_memory_order_and_refuses_others():
         mu.muon_grad_norm([t], record=torch.zeros(3, device="cuda"))
 
 
+@pytest.mark.parametrize("limit", [0.01, 1e6])
+def test_clip_agrees_with_torch_on_a_model(limit):
+    """An independent implementation: torch.nn.utils.clip_grad_norm_ in fp64 on
+    the CPU, on the gradients of a small model.  Three roundings to fp32 lie
+    between them (the norm is not one of them): the factor, the product, and
+    the limit's own."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    torch.manual_seed(73)
+    model = torch.nn.Sequential(torch.nn.Embedding(50, 24), torch.nn.Linear(24, 72), torch.nn.GELU(),
+                                torch.nn.LayerNorm(72), torch.nn.Linear(72, 50)).cuda()
+    out = model(torch.randint(0, 50, (8, 16), device="cuda"))
+    torch.nn.functional.cross_entropy(out.view(-1, 50), torch.randint(0, 50, (128,), device="cuda")).backward()
+    params = list(model.parameters())
+    twins = [torch.nn.Parameter(p.detach().double().cpu()) for p in params]
+    for p, t in zip(params, twins):
+        t.grad = p.grad.double().cpu()
+    norm = torch.nn.utils.clip_grad_norm_(twins, limit).item()
+    record = mu.muon_grad_clip([p.grad for p in params], limit)
+    assert abs(record[0].item() - norm) <= HALF_STEP * norm
+    for p, t in zip(params, twins):
+        err = (p.grad.double().cpu() - t.grad).abs()
+        assert (err <= 3.1 * 2.0 ** -24 * t.grad.abs() + 2.0 ** -149).all()
+
+
 def test_two_streams_at_once():
     """Calls on two streams overlap: each has a workspace of its own."""
     torch = torch_mod()

@@ -106,6 +106,17 @@ def test_binding_refuses():
         mu.muon_adamw_step([cpu.bfloat16()], [cpu.bfloat16()], [cpu], [cpu], 1e-3)
 
 
+def test_binding_fails_loudly_without_its_calls(monkeypatch):
+    import sys
+
+    import optimizer_muon_step_amd as mu
+    monkeypatch.setattr(_lib, "_tensor_calls", None)
+    monkeypatch.delattr(mu, "_tensor_calls", raising=False)
+    monkeypatch.setitem(sys.modules, "optimizer_muon_step_amd._tensor_calls", None)
+    with pytest.raises(RuntimeError, match="no fallback"):
+        mu.muon_grad_norm([])
+
+
 def test_dense_layouts():
     import torch
 
