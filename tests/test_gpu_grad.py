@@ -99,6 +99,19 @@ def test_norm_same_bits_every_time():
         assert torch.equal(_bits(mu.muon_grad_norm(g, 1.0)), _bits(first))
 
 
+def test_norm_never_takes_partials_of_an_earlier_call():
+    """Calls on g and 2 g in turn, without a wait: a partial left from the call
+    before would show, since the two norms are exactly a factor of 2 apart."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    for sizes in ([40_000], [300_000, 77], [9_000_001, 3, 400_000], [5000] * 600):
+        one = _make(np.random.default_rng(74), sizes, ["fp32"])
+        two = [2 * t for t in one]
+        want = mu.muon_grad_norm(one)[0].item()
+        got = torch.stack([mu.muon_grad_norm(two if k % 2 else one)[0] for k in range(300)])
+        assert torch.equal(got.cpu(), torch.tensor([want, 2 * want] * 150)), sizes
+
+
 def test_norm_counts_a_repeated_tensor_each_time_and_leaves_gradients():
     torch = torch_mod()
     import optimizer_muon_step_amd as mu
