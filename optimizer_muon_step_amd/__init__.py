@@ -111,6 +111,7 @@ def _coeff_arg(coeffs, ns_steps):
 def _update_ptrs(updates, params):
     if updates is None:
         return None
+    updates = list(updates)
     if len(updates) != len(params):
         raise ValueError("updates must have one entry per matrix")
     ptrs = []
@@ -134,6 +135,7 @@ def muon_step(params, grads, momentum, lr=0.02, beta=0.95, ns_steps=5, coeffs=DE
     receiving the applied update.  `clip`, if given, is the record of
     muon_grad_norm: the step then takes the gradients clipped, and changes
     nothing when the record's norm is not finite."""
+    params, grads, momentum = list(params), list(grads), list(momentum)  # this call's own, whatever becomes of the lists
     n = len(params)
     if len(grads) != n or len(momentum) != n:
         raise ValueError("params, grads and momentum must have the same length")

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cstring>
 #include <exception>
+#include <new>
 #include <string>
 #include <utility>
 #include <vector>
@@ -52,9 +53,21 @@ struct Refused : std::exception {
   const char* what() const noexcept override { return text.c_str(); }
 };
 
+// The items of a list or tuple as a tuple that nothing changes (runs no Python code).
+PyObject* held_tuple(PyObject* list) {
+  PyObject* t = PyList_Check(list) ? PyList_AsTuple(list) : PyTuple_GetSlice(list, 0, PyTuple_GET_SIZE(list));
+  if (!t) {
+    PyErr_Clear();
+    throw std::bad_alloc();
+  }
+  return t;
+}
+
 std::string at_index(const char* what, size_t i) { return std::string(what) + "[" + std::to_string(i) + "]: "; }
 
-// A list or tuple of tensors taken flat.  Keeps the sequence while it lives.
+// A list or tuple of tensors taken flat, as it is now: it is copied into a
+// tuple of the call's own, which holds the tensors until the library has
+// enqueued their use and keeps its length whatever becomes of the list.
 struct TensorList {
   PyObject* seq;
   const char* what;
@@ -64,8 +77,7 @@ struct TensorList {
 
   TensorList(PyObject* list, const char* name, bool any_type, bool dense, int device) : seq(nullptr), what(name) {
     if (!PyList_Check(list) && !PyTuple_Check(list)) throw Refused(std::string(name) + ": expected a list of tensors");
-    seq = list;
-    Py_INCREF(seq);
+    seq = held_tuple(list);
     try {
       read(any_type, dense, device);
     } catch (...) {
@@ -73,21 +85,21 @@ struct TensorList {
       throw;
     }
   }
-  ~TensorList() { Py_XDECREF(seq); }
+  ~TensorList() { Py_DECREF(seq); }
   TensorList(const TensorList&) = delete;
   TensorList& operator=(const TensorList&) = delete;
 
-  size_t size() const { return (size_t)PySequence_Fast_GET_SIZE(seq); }
-  const at::Tensor& tensor(size_t i) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(seq, (Py_ssize_t)i)); }
+  size_t size() const { return ptr.size(); }
+  const at::Tensor& tensor(size_t i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(seq, (Py_ssize_t)i)); }
 
  private:
   void read(bool any_type, bool dense, int device) {
-    const size_t n = size();
+    const size_t n = (size_t)PyTuple_GET_SIZE(seq);
     ptr.resize(n);
     numel.resize(n);
     type.resize(n);
     for (size_t i = 0; i < n; ++i) {
-      if (!THPVariable_Check(PySequence_Fast_GET_ITEM(seq, (Py_ssize_t)i))) throw Refused(at_index(what, i) + "expected a tensor");
+      if (!THPVariable_Check(PyTuple_GET_ITEM(seq, (Py_ssize_t)i))) throw Refused(at_index(what, i) + "expected a tensor");
       const at::Tensor& t = tensor(i);
       const int code = type_code(t);
       if (code < 0 || (code > 0 && !any_type))
@@ -195,28 +207,47 @@ PyObject* grad_clip(PyObject*, PyObject* args) {
   });
 }
 
-// The weight decays of n tensors: one value, or a sequence of them.
-std::vector<float> decays_of(PyObject* o, size_t n) {
-  if (!PyList_Check(o) && !PyTuple_Check(o)) {
+// The weight decays of a step: one value, or a sequence of them.  Reading a
+// value may run Python code (its __float__), so they are read before any list
+// of tensors, and from a tuple of the call's own.
+struct Decays {
+  std::vector<float> values;
+  bool one;
+
+  explicit Decays(PyObject* o) : one(!PyList_Check(o) && !PyTuple_Check(o)) {
+    if (one) {
+      values.resize(1);
+      if (!number(o, &values[0])) throw Refused("weight_decay: expected one value or one per tensor");
+      return;
+    }
+    const Held held{held_tuple(o)};
+    values.resize((size_t)PyTuple_GET_SIZE(held.seq));
+    for (size_t i = 0; i < values.size(); ++i)
+      if (!number(PyTuple_GET_ITEM(held.seq, (Py_ssize_t)i), &values[i]))
+        throw Refused(at_index("weight_decay", i) + "expected a number");
+  }
+
+  // Those of n tensors.
+  void fit(size_t n) {
+    if (one) values.assign(n, values[0]);
+    if (values.size() != n) throw Refused("weight_decay: expected one value or one per tensor");
+  }
+
+ private:
+  struct Held {
+    PyObject* seq;
+    ~Held() { Py_DECREF(seq); }
+  };
+  static bool number(PyObject* o, float* value) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) {
       PyErr_Clear();
-      throw Refused("weight_decay: expected one value or one per tensor");
+      return false;
     }
-    return std::vector<float>(n, (float)v);
+    *value = (float)v;
+    return true;
   }
-  if ((size_t)PySequence_Fast_GET_SIZE(o) != n) throw Refused("weight_decay: expected one value or one per tensor");
-  std::vector<float> wd(n);
-  for (size_t i = 0; i < n; ++i) {
-    const double v = PyFloat_AsDouble(PySequence_Fast_GET_ITEM(o, (Py_ssize_t)i));
-    if (v == -1.0 && PyErr_Occurred()) {
-      PyErr_Clear();
-      throw Refused(at_index("weight_decay", i) + "expected a number");
-    }
-    wd[i] = (float)v;
-  }
-  return wd;
-}
+};
 
 // adamw_clip(params, grads, exp_avg, exp_avg_sq, weight_decay, lr, beta1, beta2, eps, step, record or None, device, stream) -> code
 PyObject* adamw_clip(PyObject*, PyObject* args) {
@@ -229,6 +260,7 @@ PyObject* adamw_clip(PyObject*, PyObject* args) {
                         &device, &stream))
     return nullptr;
   return guarded([&]() -> PyObject* {
+    Decays wd(wl);
     const TensorList p(pl, "params", false, false, device), g(gl, "grads", true, false, device);
     const TensorList u(ul, "exp_avg", false, false, device), v(vl, "exp_avg_sq", false, false, device);
     if (g.size() != p.size() || u.size() != p.size() || v.size() != p.size())
@@ -236,12 +268,12 @@ PyObject* adamw_clip(PyObject*, PyObject* args) {
     for (size_t i = 0; i < p.size(); ++i)
       if (g.numel[i] != p.numel[i] || u.numel[i] != p.numel[i] || v.numel[i] != p.numel[i])
         throw Refused("tensor " + std::to_string(i) + ": element counts differ");
-    const std::vector<float> wd = decays_of(wl, p.size());
+    wd.fit(p.size());
     const float* record = record_ptr(given, device);
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = muon_adamw_step_clip((float* const*)p.ptr.data(), g.ptr.data(), g.type.data(), (float* const*)u.ptr.data(),
-                              (float* const*)v.ptr.data(), p.numel.data(), wd.data(), (int)p.size(), lr, beta1, beta2,
+                              (float* const*)v.ptr.data(), p.numel.data(), wd.values.data(), (int)p.size(), lr, beta1, beta2,
                               eps, step, record, (hipStream_t)(uintptr_t)stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);

@@ -378,6 +378,34 @@ def test_two_threads_on_one_stream():
         assert len(got[k]) == 50 and all(torch.equal(_bits(r), _bits(want[k])) for r in got[k])
 
 
+def test_a_list_that_another_thread_changes():
+    """Tensors of zeros come and go while the calls run: each call takes the
+    list as it was at one time, and the norm is the same."""
+    import threading
+
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    grads = _make(np.random.default_rng(75), [5000, 77, 300_001], ["fp32"])
+    want = mu.muon_grad_norm(grads)
+    zeros, done = [torch.zeros(3, device="cuda") for _ in range(300)], threading.Event()
+
+    def work():
+        while not done.is_set():
+            grads.extend(zeros)
+            del grads[3:]
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    try:
+        got = [mu.muon_grad_norm(grads) for _ in range(200)]
+    finally:
+        done.set()
+        thread.join()
+    # longer lists may take another split of the sum: half a step on either side
+    got = torch.stack(got).cpu().numpy().astype(np.float64)[:, 0]
+    assert (np.abs(got - want[0].item()) <= 2 * HALF_STEP * want[0].item()).all()
+
+
 def test_captured_norm_and_clip_without_an_earlier_call():
     """Captured at once, replayed with new gradients and eager work between;
     two graphs replayed in turn."""

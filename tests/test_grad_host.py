@@ -145,3 +145,52 @@ def test_oracle_closed_forms():
     # halves and ties of the 16-bit roundings
     assert go.rounded(np.float32(1 + 2.0 ** -8), "bf16") == 1.0 and go.rounded(np.float32(1 + 3 * 2.0 ** -8), "bf16") == 1 + 2.0 ** -6
     assert go.rounded(np.float32(70000), "fp16") == np.inf and go.rounded(np.float32(2.0 ** -25), "fp16") == 0.0
+
+
+class _Meddler:
+    """A number whose reading changes a list of the call that reads it."""
+
+    def __init__(self, change):
+        self.change = change
+
+    def __float__(self):
+        self.change()
+        return 0.5
+
+
+def test_lists_that_change_while_a_call_reads_them(lib):
+    """A call goes by its lists as they were when it read them: their lengths
+    and their tensors stay the call's own."""
+    import torch
+
+    import optimizer_muon_step_amd as mu
+    calls = _lib.load_tensor_calls()
+    for k in range(4):
+        lists = [[], [], [], []]
+        wd = _Meddler(lambda: lists[k].append(torch.zeros(3)))  # noqa: B023
+        adamw = lambda: calls.adamw_clip(*lists, wd, 1e-3, 0.9, 0.999, 1e-8, 1, None, -1, 0)  # noqa: B023,E731
+        with pytest.raises(ValueError, match="on the GPU|same length"):
+            adamw()  # the decays are read first: the lists are as they are now
+    # decays that their own reading shortens: the call's are those it was given
+    decays = [0.1, 0.2]
+    decays[0] = _Meddler(decays.clear)
+    with pytest.raises(ValueError, match="one value or one per tensor"):
+        calls.adamw_clip([], [], [], [], decays, 1e-3, 0.9, 0.999, 1e-8, 1, None, -1, 0)
+    params = []
+    coeffs = (_Meddler(lambda: params.append(torch.zeros(3, 3))), 0.0, 0.0)
+    mu.muon_step(params, [], [], coeffs=coeffs, updates=[], stream=0)
+
+
+def test_refused_calls_give_back_their_references(lib):
+    import sys
+
+    import torch
+    t = torch.zeros(2)
+    tensors = [t]
+    before = sys.getrefcount(t), sys.getrefcount(tensors)
+    for _ in range(3):
+        for grads in (tensors, (t,)):
+            with pytest.raises(ValueError, match="on the GPU"):
+                _lib.load_tensor_calls().grad_norm(grads, 1.0, 1.0, None, 0, -1, 0)
+        del grads
+    assert (sys.getrefcount(t), sys.getrefcount(tensors)) == before
