@@ -242,32 +242,45 @@ def _record_ptr(record):
     return record.data_ptr()
 
 
+def _refuse_per_thread(handle):
+    if handle == 2:
+        raise ValueError("stream: hipStreamPerThread is another stream in every host thread; pass a stream of your own")
+
+
 def _on_stream(stream):
     """A context in which `stream` is torch's current one, so that what a call
     allocates belongs to the stream that uses it."""
     import torch
     if isinstance(stream, int):
+        _refuse_per_thread(stream)
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 
-# One norm workspace per device and stream: calls on one stream are ordered,
-# so each finds it as the one before left it; calls on two streams share none.
+# One norm workspace per device and stream of torch's own: calls on one stream
+# are ordered, so each finds it as the one before left it; calls on two
+# streams share none.  torch's streams are never destroyed, so these handles
+# never come to name another stream, and they are few.
 _norm_workspaces = {}
 
 
 def _norm_workspace(dev, handle):
     """The workspace of a norm on torch's current stream.  A captured call
     takes one of its own from the graph's memory, cleared by the graph, so
-    that graphs share none either."""
+    that graphs share none either; so does a call on a stream that is not
+    torch's own, whose handle may name another stream by the next call."""
     import torch
+    _refuse_per_thread(handle)
     if dev < 0:
         return torch.empty(0)
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
     ws = _norm_workspaces.get((dev, handle))
     if ws is None:
-        ws = _norm_workspaces[dev, handle] = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
+        ws = torch.zeros(GRAD_WORKSPACE_BYTES // 8, dtype=torch.float64, device=dev)
+        # the id of a stream that torch did not make is its handle
+        if handle == 0 or torch.cuda.current_stream(dev).stream_id != handle:
+            _norm_workspaces[dev, handle] = ws
     return ws
 
 
@@ -322,7 +335,9 @@ def muon_grad_norm(grads, max_norm=float("inf"), scale=1.0, record=None, stream=
     gradient accumulation, 1 / loss scale under loss scaling.  Pass the result
     as `clip` to muon_step and muon_adamw_step, which then take the gradients
     clipped without a pass that writes them back.  `record` is a tensor of 2
-    to fill instead of a new one."""
+    to fill instead of a new one.  `stream`, if not torch's current one, is a
+    torch stream or a raw handle, of a stream that lives until the call's work
+    is done; hipStreamPerThread is refused."""
     if stream is not None:
         with _on_stream(stream):
             return muon_grad_norm(grads, max_norm, scale, record)
@@ -339,7 +354,7 @@ def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=No
     factor of muon_grad_norm, in place, or rounded into `outs`, tensors of the
     same shapes and memory order and of any of the three types (16-bit
     gradients into float32 ones, say).  Returns the record {norm, factor};
-    the norm is the one before clipping."""
+    the norm is the one before clipping.  `stream` as in muon_grad_norm."""
     if stream is not None:
         with _on_stream(stream):
             return muon_grad_clip(grads, max_norm, scale, outs, record)

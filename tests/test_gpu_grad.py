@@ -352,6 +352,38 @@ def test_two_streams_at_once():
     assert torch.equal(_bits(record), _bits(want[0]))
 
 
+def test_streams_that_are_not_torchs():
+    """Streams made elsewhere come and go; no call leaves a workspace behind."""
+    import ctypes
+
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    hip = mu._lib.load()  # the HIP runtime that the library is linked against
+    grads = _make(np.random.default_rng(76), [700_001, 5, 1000], KINDS)
+    want = mu.muon_grad_norm(grads, 1.0)
+    kept = set(mu._norm_workspaces)
+    for _ in range(3):
+        handle = ctypes.c_void_p()
+        assert hip.hipStreamCreate(ctypes.byref(handle)) == 0
+        torch.cuda.synchronize()
+        got = [mu.muon_grad_norm(grads, 1.0, stream=handle.value) for _ in range(4)]
+        got.append(mu.muon_grad_norm(grads, 1.0, stream=torch.cuda.ExternalStream(handle.value)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(_bits(r), _bits(want)) for r in got)
+        assert hip.hipStreamDestroy(handle) == 0
+    assert set(mu._norm_workspaces) == kept
+    with pytest.raises(ValueError, match="hipStreamPerThread"):
+        mu.muon_grad_clip(grads, 1.0, stream=torch.cuda.ExternalStream(2))
+    # a stream of torch's keeps one workspace, by object or by handle
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (stream, stream.cuda_stream, stream):
+        record = mu.muon_grad_norm(grads, 1.0, stream=s)
+        stream.synchronize()
+        assert torch.equal(_bits(record), _bits(want))
+    assert len(set(mu._norm_workspaces) - kept) == 1
+
+
 def test_two_threads_on_one_stream():
     """Both threads' calls take the stream's one workspace, and several
     launches each: a call's launches stay together."""

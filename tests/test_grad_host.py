@@ -194,3 +194,42 @@ def test_refused_calls_give_back_their_references(lib):
                 _lib.load_tensor_calls().grad_norm(grads, 1.0, 1.0, None, 0, -1, 0)
         del grads
     assert (sys.getrefcount(t), sys.getrefcount(tensors)) == before
+
+
+def test_workspaces_are_kept_only_for_streams_that_stay(monkeypatch):
+    """torch's own streams live as long as the process, so a handle of theirs
+    names one stream.  Another handle may come to name a later stream while
+    the earlier one's norm still runs: its calls share no workspace."""
+    import types
+
+    import torch
+
+    import optimizer_muon_step_amd as mu
+    zeros, current = torch.zeros, types.SimpleNamespace(stream_id=0)
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current)
+    monkeypatch.setattr(mu, "_norm_workspaces", {})
+    for handle, stream_id in ((0, 0), (0x5000, 35), (0x5010, 67)):  # the default stream and two of the pool's
+        current.stream_id = stream_id
+        assert mu._norm_workspace(0, handle) is mu._norm_workspace(0, handle)
+        assert mu._norm_workspace(0, handle) is not mu._norm_workspace(1, handle)
+    kept = dict(mu._norm_workspaces)
+    for handle in (1, 0x7000):  # handles from elsewhere: torch takes the handle as the id
+        current.stream_id = handle
+        first, second = mu._norm_workspace(0, handle), mu._norm_workspace(0, handle)
+        assert first is not second and first.count_nonzero() == 0
+    assert mu._norm_workspaces == kept
+    # one of the pool's streams under its raw handle is the same stream
+    current.stream_id = 0x5000
+    assert mu._norm_workspace(0, 0x5000) is kept[0, 0x5000]
+
+
+def test_the_per_thread_stream_is_refused():
+    """Handle 2, hipStreamPerThread, is another stream in every host thread,
+    but one stream to the allocator that a call takes its memory from."""
+    import optimizer_muon_step_amd as mu
+    for call in (lambda: mu.muon_grad_norm([], stream=2), lambda: mu.muon_grad_clip([], 1.0, stream=2),
+                 lambda: mu._norm_workspace(0, 2)):
+        with pytest.raises(ValueError, match="hipStreamPerThread"):
+            call()
