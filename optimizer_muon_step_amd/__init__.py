@@ -215,13 +215,15 @@ def muon_newton_schulz(xs, outs, ns_steps=5, coeffs=DEFAULT_COEFFS, stream=None)
     _check(rc)
 
 
-def _fp32_flat(t, what):
+def _fp32_flat(t, what, i=None):
     import torch
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    # put together for a refusal alone: names of every tensor were 49 of 337 us of a call on 148 tensors
+    where = what if i is None else f"{what}[{i}]"
     if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{what}: expected a tensor")
-    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous float32 tensor on the GPU")
-    return t.data_ptr()
+        raise ValueError(f"{where}: expected a tensor")
+    raise ValueError(f"{where}: expected a contiguous float32 tensor on the GPU")
 
 
 def _any_16_bit(ts):
@@ -315,7 +317,7 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr, betas=(0.9, 0.999), 
         ts = (params[i], grads[i], exp_avg[i], exp_avg_sq[i])
         names = ("params", "grads", "exp_avg", "exp_avg_sq")
         for k, (t, name) in enumerate(zip(ts, names)):
-            ptrs[k].append(_fp32_flat(t, f"{name}[{i}]"))
+            ptrs[k].append(_fp32_flat(t, name, i))
         if len({t.numel() for t in ts}) != 1:
             raise ValueError(f"tensor {i}: element counts differ")
         numels.append(params[i].numel())

@@ -233,3 +233,18 @@ def test_the_per_thread_stream_is_refused():
                  lambda: mu._norm_workspace(0, 2)):
         with pytest.raises(ValueError, match="hipStreamPerThread"):
             call()
+
+
+def test_the_plain_adamw_step_names_the_tensor_it_refuses():
+    import torch
+
+    import optimizer_muon_step_amd as mu
+    t = torch.zeros(4)
+    for lists, text in ((([t],) * 4, "params[0]: expected a contiguous float32 tensor on the GPU"),
+                        (([3], [t], [t], [t]), "params[0]: expected a tensor")):
+        with pytest.raises(ValueError) as refusal:
+            mu.muon_adamw_step(*lists, 1e-3)
+        assert str(refusal.value) == text
+    with pytest.raises(ValueError) as refusal:
+        mu.muon_adamw_untie(t, t, t)
+    assert str(refusal.value) == "param: expected a contiguous float32 tensor on the GPU"
