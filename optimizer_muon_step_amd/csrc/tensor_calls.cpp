@@ -143,13 +143,20 @@ PyObject* guarded(F&& body) {
   return nullptr;
 }
 
+// Autograd takes t as changed, as after one of torch's in-place operations.
+void mark_written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // (record given or new, code of the call) as Python has it.
 PyObject* finish(PyObject* given, const at::Tensor& fresh, int rc) {
   PyObject* record = given;
   if (given == Py_None)
     record = THPVariable_Wrap(fresh);
-  else
+  else {
+    if (rc == MUON_OK) mark_written(THPVariable_Unpack(given));
     Py_INCREF(given);
+  }
   return record ? Py_BuildValue("(iN)", rc, record) : nullptr;
 }
 
@@ -203,6 +210,8 @@ PyObject* grad_clip(PyObject*, PyObject* args) {
     rc = muon_grad_clip(g.ptr.data(), o.ptr.data(), g.numel.data(), g.type.data(), o.type.data(), (int)g.size(),
                         max_norm, scale, record, (void*)(uintptr_t)ws, (hipStream_t)(uintptr_t)stream);
     Py_END_ALLOW_THREADS
+    if (rc == MUON_OK)
+      for (size_t i = 0; i < o.size(); ++i) mark_written(o.tensor(i));
     return finish(given, fresh, rc);
   });
 }

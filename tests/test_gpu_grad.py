@@ -303,6 +303,36 @@ def test_clip_keeps_memory_order_and_refuses_others():
         mu.muon_grad_norm([t], record=torch.zeros(3, device="cuda"))
 
 
+def test_autograd_notices_a_clip():
+    """What a clip writes counts as changed, as after torch's own in-place
+    operations: a backward pass through values saved before is refused."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    for n in (300, 200_001):  # one launch and two
+        x = torch.full((n,), 2.0, device="cuda", requires_grad=True)
+        (grad,) = torch.autograd.grad((x * x * x).sum(), x, create_graph=True)
+        loss = (grad * grad).sum()  # saves grad
+        version, still = grad._version, x._version
+        with pytest.raises(mu.MuonError):
+            mu.muon_grad_clip([grad], -1.0)
+        assert grad._version == version
+        mu.muon_grad_norm([grad])
+        assert grad._version == version
+        mu.muon_grad_clip([grad], 1.0)
+        assert grad._version == version + 1 and x._version == still
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        source, out, record = torch.ones(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+        mu.muon_grad_clip([source], 1.0, outs=[out], record=record)
+        assert (source._version, out._version, record._version) == (0, 1, 1)
+        mu.muon_grad_norm([source], record=record)
+        assert record._version == 2
+        with torch.inference_mode():  # tensors without a counter
+            quiet = torch.ones(n, device="cuda")
+            mu.muon_grad_clip([quiet], 1.0, record=torch.empty(2, device="cuda"))
+        assert quiet[0].item() < 1.0
+
+
 @pytest.mark.parametrize("limit", [0.01, 1e6])
 def test_clip_agrees_with_torch_on_a_model(limit):
     """An independent implementation: torch.nn.utils.clip_grad_norm_ in fp64 on
