@@ -1,6 +1,7 @@
 """Build libmuon.so (the gfx950 HIP kernels and the C ABI) in place with
-hipcc, the plain C caller muon_c_example linked against it, and the binding's
-calls on tensor lists."""
+hipcc, the plain C caller muon_c_example linked against it, and, where torch,
+Python's headers and a host C++ compiler are there, the binding's calls on
+tensor lists."""
 from __future__ import annotations
 
 import hashlib
@@ -111,8 +112,29 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB,
     os.replace(tmp, out)
     if out == LIB:
         build_c_example(verbose)
-        build_tensor_calls(verbose)
+        lacking = tensor_calls_lack()
+        if lacking is None:
+            build_tensor_calls(verbose)
+        else:
+            # the library and its C ABI stand without them; the binding's calls
+            # that need them raise, rather than use an earlier build's
+            if os.path.exists(TENSOR_CALLS):
+                os.remove(TENSOR_CALLS)
+            sys.stderr.write(f"{os.path.basename(TENSOR_CALLS)} is not built: no {lacking}\n")
     return out
+
+
+def tensor_calls_lack() -> str | None:
+    """What build_tensor_calls needs and this machine does not have, if anything."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    if not (shutil.which("g++") or shutil.which("c++")):
+        return "host C++ compiler"
+    return None
 
 
 def build_tensor_calls(verbose: bool = False) -> str:
@@ -120,8 +142,6 @@ def build_tensor_calls(verbose: bool = False) -> str:
     and libmuon.so."""
     import torch
     cxx = shutil.which("g++") or shutil.which("c++")
-    if not cxx:
-        raise RuntimeError("no host C++ compiler")
     at = os.path.dirname(torch.__file__)
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     tmp = TENSOR_CALLS + ".tmp"

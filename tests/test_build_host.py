@@ -34,3 +34,29 @@ def test_library_holds_gfx950_code():
         data = f.read()
     assert b".hip_fatbin" in data                   # the device-code section
     assert b"amdgcn-amd-amdhsa--gfx950" in data     # a code object for gfx950
+
+
+@pytest.mark.parametrize("missing", ["torch", "compiler", "headers"])
+def test_the_library_builds_without_what_only_the_binding_needs(missing, monkeypatch, tmp_path, capsys):
+    """libmuon.so and its C ABI need neither torch, nor Python's headers, nor a
+    C++ host compiler.  Without one of them the binding's tensor calls are left
+    out, with a notice; calls of an earlier build do not stay beside a new library."""
+    import shutil
+    import sys
+    import sysconfig
+    stale = tmp_path / "_tensor_calls.so"
+    stale.write_bytes(b"")
+    monkeypatch.setattr(b, "SOURCES", ["plan_host.cpp"])
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libmuon.so"))
+    monkeypatch.setattr(b, "TENSOR_CALLS", str(stale))
+    monkeypatch.setattr(b, "build_c_example", lambda verbose=False: "")
+    if missing == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    elif missing == "compiler":
+        monkeypatch.setattr(shutil, "which", lambda name: None)
+    else:
+        paths = sysconfig.get_paths()
+        monkeypatch.setattr(sysconfig, "get_paths", lambda: {**paths, "include": str(tmp_path)})
+    assert b.build(out=b.LIB) == b.LIB and os.path.exists(b.LIB)
+    assert not stale.exists()
+    assert "_tensor_calls.so" in capsys.readouterr().err
