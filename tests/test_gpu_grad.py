@@ -253,6 +253,75 @@ def test_small_clips(kind_in, kind_out, offset):
                 assert np.array_equal(_values(b).view(np.uint32), want.view(np.uint32)), (sizes, limit)
 
 
+def _device_record(grads, max_norm, scale=1.0):
+    """The record from sums in fp64 on the device, for lists that are long on the CPU."""
+    total = sum(float(piece.double().square().sum()) for g in grads for piece in g.split(1 << 24))
+    norm = scale * math.sqrt(total)
+    return norm, scale * min(1.0, max_norm / (norm + 1e-6))
+
+
+@pytest.mark.parametrize("kinds,kinds_out", [(("fp32",), ("bf16",)), (("bf16", "fp16"), ("fp32",)), (KINDS, ("fp16", "fp32", "bf16"))])
+def test_clip_into_other_tensors_past_a_whole_group_of_runs(kinds, kinds_out):
+    """Enough chunks of 4096 for one group of 8 runs of 64 and a rest that no
+    multiple of 8 fills, over tensors that begin and end anywhere in them."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    sizes = [1_500_003, 9, 700_001, 4096, 1_250_077, 40_001, 1, 8191, 333_333]
+    items = sum(-(-n // 4096) for n in sizes)
+    assert items > 8 * 64 and items % 8 and items % 64
+    rng = np.random.default_rng(77)
+    g = _make(rng, sizes, kinds, 1)
+    bufs = [torch.full((n + 5,), -7.0, dtype=_dtype(kinds_out[i % len(kinds_out)]), device="cuda") for i, n in enumerate(sizes)]
+    record = mu.muon_grad_clip(g, 3.0, scale=0.5, outs=[b[2:-3] for b in bufs])
+    got = _check_record(record, g, 3.0, 0.5)
+    for i, (t, b) in enumerate(zip(g, bufs)):
+        want = np.full(b.numel(), -7.0, np.float32)
+        want[2:-3] = go.rounded(go.clipped(_values(t), np.float32(got[1])), kinds_out[i % len(kinds_out)])
+        assert np.array_equal(_values(b).view(np.uint32), want.view(np.uint32)), i
+
+
+@pytest.mark.parametrize("sizes,kinds", [
+    ([100_000_003, 30_000_001, 5, 12_345_677, 3, 4099], ("bf16", "fp32", "fp16")),  # one launch, kept from inside it
+    ([400_001 + 2 * k for k in range(300)], KINDS),                                 # two launches, kept from inside the first
+    ([80_000_001, 70_000_003, 11], ("fp32",))])
+def test_norm_of_a_list_longer_than_what_is_kept(sizes, kinds):
+    """More than 256 MiB under a limit: the front is read one way, the end another."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    say(f"[norm long] {len(sizes)} tensors, {sum(sizes)} elements")
+    gen = torch.Generator(device="cuda").manual_seed(78)
+    g = [torch.randn(n, generator=gen, device="cuda").to(_dtype(kinds[i % len(kinds)])) for i, n in enumerate(sizes)]
+    assert sum(t.numel() * t.element_size() for t in g) > 256 << 20
+    for limit, scale in ((2.0, 0.5), (1e9, 1.0)):
+        norm, factor = _device_record(g, limit, scale)
+        got = mu.muon_grad_norm(g, limit, scale=scale).cpu().numpy().astype(np.float64)
+        assert abs(got[0] - norm) <= HALF_STEP * norm and abs(got[1] - factor) <= HALF_STEP * factor, (got, norm, factor)
+
+
+@pytest.mark.parametrize("kinds", [("fp32",), ("bf16", "fp16")])
+def test_long_clip_in_place(kinds):
+    """More chunks than an in-place launch has blocks, over several tensors:
+    each element is clipped once, and nothing beside them."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    sizes = [40_000_003, 17, 30_000_001, 4097, 5_000_001]
+    assert sum(-(-n // 4096) for n in sizes) > 16384
+    say(f"[clip long] {kinds} {sum(sizes)} elements")
+    gen = torch.Generator(device="cuda").manual_seed(79)
+    bufs = [torch.randn(n + 5, generator=gen, device="cuda").to(_dtype(kinds[i % len(kinds)])) for i, n in enumerate(sizes)]
+    g = [b[1:-4] for b in bufs]
+    before = [b.clone() for b in bufs]
+    norm, factor = _device_record(g, 1.0)
+    record = mu.muon_grad_clip(g, 1.0)
+    got = record.cpu().numpy().astype(np.float64)
+    assert abs(got[0] - norm) <= HALF_STEP * norm and abs(got[1] - factor) <= HALF_STEP * factor
+    for b, k in zip(bufs, before):
+        want = k.clone()
+        want[1:-4] = (k[1:-4].float() * record[1]).to(k.dtype)
+        assert torch.equal(b.view(torch.int32 if b.element_size() == 4 else torch.int16),
+                           want.view(torch.int32 if b.element_size() == 4 else torch.int16))
+
+
 def test_clip_scale_alone_and_many_tensors():
     """No limit: only the scale; more tensors than one launch's table holds."""
     import optimizer_muon_step_amd as mu
