@@ -35,14 +35,14 @@ constexpr int NORM_MAX_BLOCKS = 1024;    // partial sums in the workspace
 // NORM_KEEP_BYTES of a call (the memory-side cache's size) are read with plain
 // loads, which leave them in that cache, and what is before them with
 // non-temporal ones, which are faster.  Measured with 0 and with 256 MiB
-// kept: norm of 498 MB 75 and 79 us; norm and AdamW of 39.5 M elements 211
-// and 191 us, of 124 M 676 and 639 us; norm and clip of 124 M bf16 elements
-// into fp32 163 and 147 us.
+// kept: norm of 498 MB 75 and 79 us; norm and AdamW of 39.5 M elements 212
+// and 191 us, of 124 M 644 and 617 us; norm and clip of 124 M bf16 elements
+// into fp32 164 and 148 us.
 constexpr int64_t NORM_KEEP_BYTES = (int64_t)256 << 20;
 // A norm or clip of at most NORM_SMALL_ITEMS items (256 KB) is one launch of
-// one block, a wave to an item: a norm takes 6.8 us a call against 7.8 by the
-// other kernels, a clip 7.0 against 12.4, of 2 items, and 6.7 and 7.8, 7.7
-// and 12.3 of 16.
+// one block, a wave to an item: a norm takes 6.6 us a call against 7.3 by the
+// other kernels, a clip 6.6 against 11.8, of 2 items, and 6.3 and 7.4, 7.5
+// and 11.7 of 16.
 constexpr int NORM_SMALL_ITEMS = 16;
 constexpr int NORM_SMALL_THREADS = 1024;
 constexpr int NORM_GROUP = 32;  // blocks that count on one counter
@@ -51,7 +51,9 @@ constexpr int norm_chunk(int type) { return NORM_CHUNK_BYTES / grad_type_bytes(t
 
 // The caller's workspace.  `arrived` counts the blocks of a group that have
 // stored their partial sum, `groups` the groups that are complete; both are
-// zero between calls.  Each counter has a 128-byte line of its own.
+// zero between calls.  Counters are 128 bytes, a cache line, apart, so that no
+// two share a line, whatever the alignment of the workspace.  Of the
+// MUON_GRAD_WORKSPACE_BYTES that a caller gives the last 4224 are not used.
 struct NormCounter {
   uint32_t arrived;
   uint32_t pad_[31];
@@ -79,13 +81,14 @@ static_assert(sizeof(NormArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // ---- clipping ----
 // Out of place one block per item, in per-XCD runs of CLIP_RUN items; without
-// the runs and with them, norm included: 1.56 G bf16 elements 1486 and 1460
-// us, 124 M bf16 into fp32 152 and 148, 124 M fp32 227 and 226, 39.5 M fp32
-// 72 and 74.  In place a factor of 1, the usual one, ends every block at
+// the runs and with them, norm included: 1.56 G bf16 elements 1488 and 1466
+// us, 124 M bf16 into fp32 152 and 149, 124 M fp32 228 and 227, 39.5 M fp32
+// 73 and 74.  In place a factor of 1, the usual one, ends every block at
 // once, and dispatching them is then all the time there is (1.3 ns each): at
-// most CLIP_IN_PLACE_BLOCKS take the items in turn.  With a block per item
-// and with that many: 1.56 G bf16 elements below the limit 541 and 468 us,
-// clipped 1494 and 1603; 124 M fp32 elements 83 and 80, 237 and 236.
+// most CLIP_IN_PLACE_BLOCKS take the items in turn, which costs a long call
+// that does clip 7 %.  With a block per item and with that many: 1.56 G bf16
+// elements below the limit 542 and 470 us, clipped 1496 and 1607; 124 M fp32
+// elements 83 and 80, 238 and 238.
 constexpr int CLIP_CHUNK = 4096;  // elements
 constexpr int CLIP_RUN = 64;
 constexpr int CLIP_IN_PLACE_BLOCKS = 16384;
@@ -116,9 +119,9 @@ struct GradSmallArgs {
 // ---- AdamW on clipped gradients ----
 // Elements per work item: long chunks, in per-XCD runs of ADAMC_LONG_RUN, for
 // calls of at least ADAMC_LONG_MIN elements.  Measured with short and with
-// long chunks, norm included: 39.5 M fp32 elements 193 and 200 us (fewer,
-// larger blocks end less evenly), 124 M fp32 642 and 625 us, 1.56 G with bf16
-// gradients 7.5 and 7.2 ms (7.5 without the runs).
+// long chunks, norm included: 39.5 M fp32 elements 192 and 202 us (fewer,
+// larger blocks end less evenly), 124 M fp32 652 and 625 us, 1.56 G with bf16
+// gradients 7.5 and 7.2 ms (7.3 without the runs).
 constexpr int ADAMC_CHUNK = 4096, ADAMC_LONG_CHUNK = 8192;
 constexpr int ADAMC_LONG_RUN = 16;
 constexpr int64_t ADAMC_LONG_MIN = (int64_t)1 << 26;

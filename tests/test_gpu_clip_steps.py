@@ -259,6 +259,31 @@ def test_training_loop_fused_equals_clip_in_place():
         assert all(torch.equal(a, b) for a, b in zip(W + M + P + U + V, We + Me + Pe + Ue + Ve)), step
 
 
+def test_training_step_on_16_bit_gradients():
+    """muon_step takes fp32 gradients: 16-bit ones are clipped into fp32 first,
+    which gives the bits of clipping as the steps read their exact fp32 copies."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    rng = np.random.default_rng(80)
+    shapes, sizes, W, M, P, U, V = _training_state(rng)
+    We, Me, Pe, Ue, Ve = ([t.clone() for t in L] for L in (W, M, P, U, V))
+    k = len(shapes)
+    G = [to_gpu(rng.standard_normal(s).astype(np.float32)).to(_dtype(kind))
+         for s, kind in zip(shapes + [(n,) for n in sizes], ("bf16", "fp16", "bf16") * 3)]
+    record = mu.muon_grad_norm(G, 1.0)
+    before = [t.clone() for t in W + M]
+    with pytest.raises(ValueError, match=r"grads\[0\]: expected a contiguous float32 tensor"):
+        mu.muon_step(W, G[:k], M, clip=record)
+    assert all(torch.equal(a, b) for a, b in zip(W + M, before))
+    G32 = [torch.empty(t.shape, device="cuda") for t in G]
+    mu.muon_grad_clip(G, 1.0, outs=G32)
+    mu.muon_step(W, G32[:k], M, lr=0.02)
+    mu.muon_adamw_step(P, G32[k:], U, V, 6e-4, step=1)
+    mu.muon_step(We, [t.float() for t in G[:k]], Me, lr=0.02, clip=record)
+    mu.muon_adamw_step(Pe, G[k:], Ue, Ve, 6e-4, step=1, clip=record)
+    assert all(torch.equal(a, b) for a, b in zip(W + M + P + U + V, We + Me + Pe + Ue + Ve))
+
+
 def test_captured_training_step_replays_like_eager():
     torch = torch_mod()
     import optimizer_muon_step_amd as mu
