@@ -356,7 +356,8 @@ def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=No
     factor of muon_grad_norm, in place, or rounded into `outs`, tensors of the
     same shapes and memory order and of any of the three types (16-bit
     gradients into float32 ones, say).  Returns the record {norm, factor};
-    the norm is the one before clipping.  `stream` as in muon_grad_norm."""
+    the norm is the one before clipping.  Autograd takes what is written as
+    changed.  `stream` as in muon_grad_norm."""
     if stream is not None:
         with _on_stream(stream):
             return muon_grad_clip(grads, max_norm, scale, outs, record)
