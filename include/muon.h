@@ -300,6 +300,140 @@ int muon_step_clip(float* const* params, const float* const* grads, float* const
                    const muon_shape_t* shapes, int n, float lr, float beta, int ns_steps, const float* coeffs,
                    uint16_t* const* updates, const float* record, hipStream_t stream);
 
+/*
+ * Products of the hidden layers, whose weights muon_step takes: the forward
+ * product with bias, activation, dropout and residual in its epilogue, and the
+ * two products of its backward pass ("Let's reproduce GPT-2 (124M)": a block's
+ * linear layers, its MLP with the tanh form of GELU and its residual path).
+ * For a layer z = x w + bias, y = residual + drop(act(z)):
+ *   x m x k, w k x n, bias n;  z, y m x n
+ *   muon_linear      y, and z itself on request (for the backward pass)
+ *   muon_linear_dx   dx = residual + drop(dz w^T) act'(preact), m x k: the
+ *                    gradient of the layer's input, carried on through the
+ *                    dropout and activation of the layer below (preact is that
+ *                    layer's z) where they are given
+ *   muon_linear_dw   dw = x^T dz, or dw + x^T dz;  dbias likewise from the sums
+ *                    of dz over its rows
+ * Operands are bf16 or fp16; weights may also be fp32 (the master weights
+ * that muon_step steps) and are then rounded to x's type, nearest even.
+ * Everything else is fp32: the products' sums, bias, activation, its slope and
+ * the residual's sum; y, dx and z are each rounded once, nearest even.  dw and
+ * dbias are fp32.  Equal calls give equal bits.
+ *   act     MUON_ACT_GELU  z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3)
+ *           MUON_ACT_RELU  max(z, 0);  MUON_ACT_RELU2  max(z, 0)^2
+ *   drop    with t = min(65535, floor(2^16 dropout + 1/2)): an element whose 16 random
+ *           bits are at least t is kept, times 2^16 / (2^16 - t); the others become 0,
+ *           whatever they were (an infinity or NaN too).  So `dropout` acts in steps
+ *           of 2^-16.  The bits of element (r, c): of the 128 bits that Philox 4x32
+ *           (Salmon, Moraes, Dror and Shaw, SC'11) with 7 rounds makes of the
+ *           counter (c / 8, r, site, step) under the key (seed low, seed high), bits
+ *           16 (c mod 8) and up.  The mask is never stored: muon_linear_dx and
+ *           muon_dropout make it anew from the same numbers, for a matrix of the
+ *           same width.  site tells a model's dropouts apart, step the training steps.
+ *
+ * Fields of muon_linear_t (for muon_linear_dx x is dz, m x n, y is dx, m x k,
+ * residual is m x k and preact, read, m x k):
+ *   m, k, n   m 0 .. MUON_LINEAR_MAX_ROWS; k, n 1 .. MUON_LINEAR_MAX_WIDTH;
+ *             m = 0 does nothing
+ *   x, w, residual, y, preact  device; elements of a row adjacent, rows ldx, ldw,
+ *             ldr, ldy, ldp elements apart, any alignment of the element
+ *             type.  w_transposed = 1: w is stored n x k (ldw from row to row of k).
+ *             Rows that are read may overlap (a distance of 0 repeats one); rows that are
+ *             written may not.  A matrix whose base is not 16-byte aligned, whose
+ *             rows are not a multiple of 8 elements apart or long, or
+ *             which is fp32 is copied to the workspace first: x costs that pass once more.
+ *   x_type    MUON_BF16 or MUON_FP16, also the type of preact
+ *   w_type, bias_type   x_type or MUON_FP32
+ *   y_type    x_type or MUON_FP32, also the type of residual
+ *   bias, residual, preact   may be NULL; muon_linear_dx takes no bias, and
+ *             preact if and only if act is not MUON_ACT_NONE
+ *   dropout   in [0, 1)
+ *   rng       NULL, or two int64 on the device, 8-byte aligned: {seed, step}, read
+ *             when the call runs, in the place of seed and step (a captured
+ *             training step counts its step there); their bits are taken modulo
+ *             2^64 and 2^32
+ * y may be the residual itself, and for muon_linear_dx the preact (same
+ * pointer, distance and type); no other array may overlap a written one, except
+ * as column ranges of one buffer of rows.
+ * workspace: device, 16-byte aligned, of at least the bytes that the
+ * _workspace_bytes function gives for the same arguments (0: NULL will do).  Its contents
+ * mean nothing before or after a call; calls that share it must be ordered on
+ * the GPU.  The calls use none of the library's own workspace or plans: they
+ * allocate nothing, cache nothing, and can be captured without an earlier call.
+ */
+#define MUON_ACT_NONE 0
+#define MUON_ACT_GELU 1
+#define MUON_ACT_RELU 2
+#define MUON_ACT_RELU2 3
+#define MUON_LINEAR_MAX_ROWS (1 << 30)
+#define MUON_LINEAR_MAX_WIDTH (1 << 22)
+
+typedef struct {
+  int64_t m, k, n;
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* preact;
+  const int64_t* rng;
+  int64_t ldx, ldw, ldr, ldy, ldp;
+  uint64_t seed;
+  uint32_t step, site;
+  float dropout;
+  int x_type, w_type, w_transposed, bias_type, y_type;
+  int act;
+} muon_linear_t;
+
+int muon_linear(const muon_linear_t* layer, void* workspace, size_t workspace_bytes, hipStream_t stream);
+int muon_linear_dx(const muon_linear_t* layer, void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* backward: 0 for muon_linear, 1 for muon_linear_dx.  0 is also given for
+ * arguments that the call refuses. */
+size_t muon_linear_workspace_bytes(const muon_linear_t* layer, int backward);
+
+/*
+ * dw is k x n (dw_transposed = 1: stored n x k), rows lddw elements apart; dbias
+ * may be NULL.  accumulate = 1 adds to what dw and dbias hold (the
+ * micro-batches of a step).  m = 0 writes zeros, or adds nothing.
+ */
+typedef struct {
+  int64_t m, k, n;
+  const void* x;
+  const void* dz;
+  float* dw;
+  float* dbias;
+  int64_t ldx, lddz, lddw;
+  int type, dw_transposed, accumulate;
+} muon_linear_dw_t;
+
+int muon_linear_dw(const muon_linear_dw_t* layer, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t muon_linear_dw_workspace_bytes(const muon_linear_dw_t* layer);
+
+/*
+ * Dropout by itself: y = residual + drop(x) act'(preact), m x n, with the mask,
+ * the fields and the rules of muon_linear_t.  Without preact this is dropout and
+ * its gradient (the same call on dy); with it, the gradient dz of a layer's z.
+ * x_type any of the three types, also that of preact; y_type any, also that of
+ * residual; n up to MUON_DROPOUT_MAX_COLS.  y may be x, preact or residual itself.
+ */
+#define MUON_DROPOUT_MAX_COLS ((int64_t)1 << 34)
+typedef struct {
+  int64_t m, n;
+  const void* x;
+  const void* residual;
+  void* y;
+  const void* preact;
+  const int64_t* rng;
+  int64_t ldx, ldr, ldy, ldp;
+  uint64_t seed;
+  uint32_t step, site;
+  float dropout;
+  int x_type, y_type;
+  int act;
+} muon_dropout_t;
+
+int muon_dropout(const muon_dropout_t* args, hipStream_t stream);
+
 /* Thread-local description of the last failing call on this thread ("" if none). */
 const char* muon_last_error(void);
 
@@ -364,6 +498,9 @@ int muon_set_lanes(int lanes);
 #define MUON_KERNEL_ADAMW 6    /* multi-tensor AdamW (muon_adamw_step, muon_adamw_step_clip) */
 #define MUON_KERNEL_GRAD_NORM 7 /* global gradient norm */
 #define MUON_KERNEL_GRAD_CLIP 8 /* clipped gradients of muon_grad_clip */
+#define MUON_KERNEL_LINEAR 9    /* muon_linear, muon_linear_dx, with their operands' copies */
+#define MUON_KERNEL_LINEAR_DW 10 /* muon_linear_dw, likewise */
+#define MUON_KERNEL_DROPOUT 11  /* muon_dropout */
 int muon_timing_enable(int kernel);
 int muon_timing_read(double* total_ms, int64_t* launches);
 

@@ -4,8 +4,9 @@ Thin argument marshalling over the C ABI declared in include/muon.h; every
 step of the computation runs in the library's HIP kernels.  Tensors are torch
 tensors on the current HIP device: fp32 params/grads/momentum, bf16 for the
 Newton-Schulz entry; the gradients of the norm, clip and AdamW calls may be
-bf16 or fp16 too.  Calls enqueue on torch's current stream (or `stream`)
-and return without synchronising.
+bf16 or fp16 too, and the layers' products take bf16 and fp16 activations.
+Calls enqueue on torch's current stream (or `stream`) and return without
+synchronising.
 """
 from __future__ import annotations
 
@@ -16,15 +17,17 @@ from . import _lib
 __all__ = [
     "DEFAULT_COEFFS", "MuonError", "matrix_shape", "muon_step", "muon_step_noalloc", "muon_newton_schulz", "muon_adamw_step", "muon_adamw_untie",
     "muon_grad_norm", "muon_grad_clip",
+    "muon_linear", "muon_linear_dx", "muon_linear_dw", "muon_dropout",
     "muon_workspace_bytes",
     "muon_set_workspace", "muon_release", "muon_plan_stats", "muon_set_lanes", "muon_timing_enable", "muon_timing_read", "muon_last_error",
     "KERNEL_MOMENTUM", "KERNEL_CAST", "KERNEL_GRAM", "KERNEL_POLY", "KERNEL_UPDATE", "KERNEL_APPLY",
-    "KERNEL_ADAMW", "KERNEL_GRAD_NORM", "KERNEL_GRAD_CLIP",
+    "KERNEL_ADAMW", "KERNEL_GRAD_NORM", "KERNEL_GRAD_CLIP", "KERNEL_LINEAR", "KERNEL_LINEAR_DW", "KERNEL_DROPOUT",
 ]
 
 DEFAULT_COEFFS = (3.4445, -4.7750, 2.0315)
 KERNEL_MOMENTUM, KERNEL_CAST, KERNEL_GRAM, KERNEL_POLY, KERNEL_UPDATE, KERNEL_APPLY, KERNEL_ADAMW = range(7)
 KERNEL_GRAD_NORM, KERNEL_GRAD_CLIP = 7, 8
+KERNEL_LINEAR, KERNEL_LINEAR_DW, KERNEL_DROPOUT = 9, 10, 11
 GRAD_WORKSPACE_BYTES = 16640
 _CODES = {-1: "MUON_EINVAL", -2: "MUON_ENOMEM", -3: "MUON_EHIP"}
 
@@ -368,6 +371,100 @@ def muon_grad_clip(grads, max_norm, scale=1.0, outs=None, record=None, stream=No
                                                     scale, record, ws.data_ptr(), dev, handle)
     _check(rc)
     return record
+
+
+_ACTS = {None: 0, "gelu": 1, "relu": 2, "relu2": 3}
+
+
+def _act_code(act):
+    try:
+        return _ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act: {act!r} is none of None, 'gelu', 'relu', 'relu2'") from None
+
+
+def _dtype_code(dtype):
+    if dtype is None:
+        return -1
+    import torch
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if dtype not in codes:
+        raise ValueError(f"out_dtype: expected float32, bfloat16 or float16, not {dtype}")
+    return codes[dtype]
+
+
+def muon_linear(x, w, bias=None, act=None, dropout=0.0, rng=None, site=0, residual=None, out=None, out_dtype=None,
+                preact=None, stream=None):
+    """A layer's forward product: residual + drop(act(x w + bias)).
+
+    `x` is bfloat16 or float16, (..., inputs); `w` is inputs x outputs in either
+    memory order (the transposed view of an outputs x inputs weight is one),
+    of x's type or float32 (rounded to x's type).  `act` is None, 'gelu' (the
+    tanh form), 'relu' or 'relu2' (its square).  With `dropout` > 0, `rng` is
+    (seed, step), or an int64 tensor of the two on the GPU, read when the call
+    runs (under a captured graph: at every replay); `site` tells the dropouts of
+    a model apart.  The mask is never stored: the same dropout, rng and site in
+    muon_linear_dx or muon_dropout, on a matrix as wide, make it again.
+    `residual` and the result are of x's type or float32 (`out_dtype`; by default the
+    residual's type, or x's); `out` is a tensor to fill, and may be the residual.
+    `preact`, of x's type, receives x w + bias for the backward pass.  Rows may
+    lie apart in memory and start anywhere; the kernels read them in place if rows
+    are 16-byte aligned and multiples of 8 elements long, and through a copy
+    otherwise.  `stream` as in muon_grad_norm.  No autograd graph is recorded."""
+    return _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preact, 0, stream)
+
+
+def muon_linear_dx(dz, w, act=None, preact=None, dropout=0.0, rng=None, site=0, residual=None, out=None,
+                   out_dtype=None, stream=None):
+    """The gradient of a layer's input from that of its z = x w + bias:
+    residual + drop(dz w^T) act'(preact).
+
+    `act` and `preact` (both or neither), `dropout`, `rng` and `site` are those of the
+    layer whose output x is, so that the result is the gradient of that layer's z;
+    `residual` is a gradient that reaches x another way.  Types, memory
+    orders, `out` (which may be the residual or preact) and `stream` as in muon_linear."""
+    return _linear(dz, w, None, act, dropout, rng, site, residual, out, out_dtype, preact, 1, stream)
+
+
+def _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preact, backward, stream):
+    if stream is not None:
+        with _on_stream(stream):
+            return _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preact, backward, None)
+    dev = _current_device()
+    rc, y = _lib.load_tensor_calls().linear(x, w, bias, _act_code(act), dropout, rng, site, residual, out,
+                                            _dtype_code(out_dtype), preact, backward, dev,
+                                            _stream_handle(None) if dev >= 0 else 0)
+    _check(rc)
+    return y
+
+
+def muon_linear_dw(x, dz, dw, dbias=None, accumulate=False, stream=None) -> None:
+    """The gradients of a layer's weight and bias: dw = x^T dz and dbias = the sums of
+    dz over its rows, or both added to what the tensors hold (`accumulate`: the
+    micro-batches of a step).  `x` and `dz` are bfloat16 or float16, (..., inputs) and
+    (..., outputs); `dw` is float32, inputs x outputs in either memory order,
+    as muon_step reads it, and `dbias` float32, as muon_adamw_step does."""
+    if stream is not None:
+        with _on_stream(stream):
+            return muon_linear_dw(x, dz, dw, dbias, accumulate)
+    dev = _current_device()
+    _check(_lib.load_tensor_calls().linear_dw(x, dz, dw, dbias, accumulate, dev, _stream_handle(None) if dev >= 0 else 0))
+
+
+def muon_dropout(x, p, rng, site=0, act=None, preact=None, residual=None, out=None, out_dtype=None, stream=None):
+    """residual + drop(x) act'(preact), elementwise: dropout of any tensor, its
+    gradient (the same call on the gradient), or with `act` and `preact` the gradient dz of a
+    layer's z behind activation and dropout.  float32, bfloat16 or float16; the
+    mask goes by the last dimension and the rows before it, as in muon_linear.
+    `out` may be x, preact or residual."""
+    if stream is not None:
+        with _on_stream(stream):
+            return muon_dropout(x, p, rng, site, act, preact, residual, out, out_dtype)
+    dev = _current_device()
+    rc, y = _lib.load_tensor_calls().dropout(x, p, rng, site, _act_code(act), preact, residual, out,
+                                             _dtype_code(out_dtype), dev, _stream_handle(None) if dev >= 0 else 0)
+    _check(rc)
+    return y
 
 
 def muon_adamw_untie(param, exp_avg, exp_avg_sq, transpose=False, stream=None):

@@ -16,6 +16,34 @@ class MuonShape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class MuonLinear(ctypes.Structure):
+    """muon_linear_t."""
+    _fields_ = ([(f, ctypes.c_int64) for f in ("m", "k", "n")]
+                + [(f, ctypes.c_void_p) for f in ("x", "w", "bias", "residual", "y", "preact", "rng")]
+                + [(f, ctypes.c_int64) for f in ("ldx", "ldw", "ldr", "ldy", "ldp")]
+                + [("seed", ctypes.c_uint64), ("step", ctypes.c_uint32), ("site", ctypes.c_uint32),
+                   ("dropout", ctypes.c_float)]
+                + [(f, ctypes.c_int) for f in ("x_type", "w_type", "w_transposed", "bias_type", "y_type", "act")])
+
+
+class MuonLinearDw(ctypes.Structure):
+    """muon_linear_dw_t."""
+    _fields_ = ([(f, ctypes.c_int64) for f in ("m", "k", "n")]
+                + [(f, ctypes.c_void_p) for f in ("x", "dz", "dw", "dbias")]
+                + [(f, ctypes.c_int64) for f in ("ldx", "lddz", "lddw")]
+                + [(f, ctypes.c_int) for f in ("type", "dw_transposed", "accumulate")])
+
+
+class MuonDropout(ctypes.Structure):
+    """muon_dropout_t."""
+    _fields_ = ([(f, ctypes.c_int64) for f in ("m", "n")]
+                + [(f, ctypes.c_void_p) for f in ("x", "residual", "y", "preact", "rng")]
+                + [(f, ctypes.c_int64) for f in ("ldx", "ldr", "ldy", "ldp")]
+                + [("seed", ctypes.c_uint64), ("step", ctypes.c_uint32), ("site", ctypes.c_uint32),
+                   ("dropout", ctypes.c_float)]
+                + [(f, ctypes.c_int) for f in ("x_type", "y_type", "act")])
+
+
 _SHAPES = ctypes.POINTER(MuonShape)
 _FLOAT3 = ctypes.POINTER(ctypes.c_float)
 
@@ -40,6 +68,12 @@ SIGNATURES = {
                                             ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_int64, _P, _P]),
     "muon_step_clip": (ctypes.c_int, [_PP, _PP, _PP, _SHAPES, ctypes.c_int, ctypes.c_float, ctypes.c_float,
                                       ctypes.c_int, _FLOAT3, _PP, _P, _P]),
+    "muon_linear": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "muon_linear_dx": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "muon_linear_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int]),
+    "muon_linear_dw": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "muon_linear_dw_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "muon_dropout": (ctypes.c_int, [_P, _P]),
     "muon_last_error": (ctypes.c_char_p, []),
     "muon_workspace_bytes": (ctypes.c_size_t, [_SHAPES, ctypes.c_int]),
     "muon_set_workspace": (ctypes.c_int, [_P, ctypes.c_size_t]),

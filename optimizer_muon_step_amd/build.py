@@ -20,7 +20,8 @@ TENSOR_CALLS = os.path.join(HERE, "_tensor_calls.so")
 C_EXAMPLE = os.path.join(HERE, "muon_c_example")
 SOURCES = ["muon_api.hip", "muon_noalloc.hip", "plan_host.cpp", "kernels_tables.hip", "kernels_momentum.hip", "kernels_elementwise.hip",
            "kernels_ns.hip", "kernels_ns_gram.hip", "kernels_ns_fused.hip", "kernels_adamw.hip", "grad_api.hip",
-           "grad_host.cpp", "kernels_grad.hip"]
+           "grad_host.cpp", "kernels_grad.hip", "linear_api.hip", "linear_host.cpp", "kernels_linear.hip",
+           "kernels_linear_dw.hip", "kernels_dropout.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,28 @@
+// Products of a layer's forward and input-gradient pass (see linear_gemm.h).
+#include <hip/hip_runtime.h>
+
+#include "linear_gemm.h"
+#include "muon_internal.h"
+
+namespace muon {
+
+using namespace lin;
+
+template <int TYPE, bool BK>
+static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
+  const int grid = a.tiles_m * a.tiles_n * a.splits;
+  switch (tile) {
+    case LIN_TILE_128:
+      linear_gemm_kernel<TYPE, false, BK, false, 128, 128, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a);
+      break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_linear(const LinGemmArgs& a, int type, bool b_kmajor, int tile, hipStream_t s) {
+  if (type == GRAD_BF16) return b_kmajor ? launch_tile<GRAD_BF16, true>(a, tile, s) : launch_tile<GRAD_BF16, false>(a, tile, s);
+  return b_kmajor ? launch_tile<GRAD_FP16, true>(a, tile, s) : launch_tile<GRAD_FP16, false>(a, tile, s);
+}
+
+}  // namespace muon

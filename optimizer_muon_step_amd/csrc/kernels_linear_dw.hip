@@ -1,0 +1,62 @@
+// Weight-gradient products of a layer (see linear_gemm.h) and the pass that
+// adds the splits of a long reduction.
+#include <hip/hip_runtime.h>
+
+#include "linear_gemm.h"
+#include "muon_internal.h"
+
+namespace muon {
+
+using namespace lin;
+
+template <int TYPE>
+static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
+  const int grid = a.tiles_m * a.tiles_n * a.splits;
+  switch (tile) {
+    case LIN_TILE_128:
+      linear_gemm_kernel<TYPE, true, true, true, 128, 128, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a);
+      break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_dw(const LinGemmArgs& a, int type, int tile, hipStream_t s) {
+  return type == GRAD_BF16 ? launch_tile<GRAD_BF16>(a, tile, s) : launch_tile<GRAD_FP16>(a, tile, s);
+}
+
+// A thread to eight elements of a row of c, and behind them a thread to each
+// sum.  The splits are added in their order, so equal calls give equal bits.
+__global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const LinFinishArgs a) {
+  if ((int)blockIdx.x >= a.sum_first_block) {
+    const int i = ((int)blockIdx.x - a.sum_first_block) * FINISH_THREADS + threadIdx.x;
+    if (i >= a.n_sums) return;
+    float v = 0.0f;
+    for (int r = 0; r < a.sum_rows; ++r) v += gptr(a.sum_part)[r * a.sum_stride + i];
+    gptr(a.sums)[i] = a.add ? gptr(a.sums)[i] + v : v;
+    return;
+  }
+  const int eights = (a.n + 7) >> 3;
+  const int64_t i = (int64_t)blockIdx.x * FINISH_THREADS + threadIdx.x;
+  const int64_t row = i / eights;
+  if (row >= a.m) return;
+  const int col = (int)(i - row * eights) * 8, have = min(8, a.n - col);
+  f32x8 v = load8<GRAD_FP32>(a.part, row * a.part_ld + col);  // its rows are padded to whole tiles
+  for (int s = 1; s < a.splits; ++s) v += load8<GRAD_FP32>(a.part + s * a.part_stride, row * a.part_ld + col);
+  const GradStore store = {a.c, a.ldc, a.add != 0};
+  if (have == 8) {
+    store(row, col, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k < have) store.one(row, col + k, v[k]);
+  }
+}
+
+hipError_t launch_linear_finish(const LinFinishArgs& a, hipStream_t s) {
+  const int blocks = a.sum_first_block + (a.n_sums + FINISH_THREADS - 1) / FINISH_THREADS;
+  linear_finish_kernel<<<blocks, FINISH_THREADS, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -1,0 +1,393 @@
+// Validation and launch arguments of the hidden layers' products and of
+// dropout.  No GPU calls.
+#include "linear_host.h"
+
+#include <algorithm>
+#include <cmath>
+
+#include "plan_host.h"
+
+namespace muon {
+
+static_assert(LIN_ACT_NONE == MUON_ACT_NONE && LIN_ACT_GELU == MUON_ACT_GELU && LIN_ACT_RELU == MUON_ACT_RELU &&
+                  LIN_ACT_RELU2 == MUON_ACT_RELU2, "activation codes");
+
+namespace {
+
+constexpr int64_t MAX_WIDTH = MUON_LINEAR_MAX_WIDTH;
+constexpr int64_t MAX_ROWS = MUON_LINEAR_MAX_ROWS;
+constexpr int64_t MAX_BYTES = (int64_t)1 << 46;  // of one matrix, gaps between its rows included
+
+// A matrix of a call: rows of `cols` elements, ld elements apart.
+struct Matrix {
+  const char* what;
+  const void* p;
+  int64_t rows, cols, ld;
+  int type;
+  bool written;
+
+  uintptr_t lo() const { return (uintptr_t)p; }
+  uint64_t size() const { return grad_type_bytes(type); }
+  uintptr_t hi() const { return lo() + (uint64_t)((rows - 1) * ld + cols) * size(); }
+  bool is(const Matrix& o) const { return p == o.p && type == o.type && (ld == o.ld || rows == 1); }
+};
+
+int check_dim(int64_t v, int64_t least, int64_t most, const char* what) {
+  if (v < least || v > most)
+    return fail(MUON_EINVAL, "%s = %lld outside [%lld, %lld]", what, (long long)v, (long long)least, (long long)most);
+  return MUON_OK;
+}
+
+int check_matrix(const Matrix& m) {
+  if (m.type < MUON_FP32 || m.type > MUON_FP16)
+    return fail(MUON_EINVAL, "%s: type %d is no element type (MUON_FP32, MUON_BF16, MUON_FP16)", m.what, m.type);
+  if (!m.p) return fail(MUON_EINVAL, "%s is NULL", m.what);
+  if (m.lo() % m.size()) return fail(MUON_EINVAL, "%s is not %d-byte aligned", m.what, (int)m.size());
+  if (m.rows > 1 && (m.written ? m.ld < m.cols : m.ld < 0))
+    return fail(MUON_EINVAL, "%s: rows %lld elements apart%s", m.what, (long long)m.ld,
+                m.written ? " overlap" : "");
+  if (m.rows > 1 && m.ld > MAX_BYTES / 4 / m.rows)
+    return fail(MUON_EINVAL, "%s: rows %lld elements apart are too far", m.what, (long long)m.ld);
+  return MUON_OK;
+}
+
+// Two matrices that share an element.  Column ranges of one buffer do not.
+bool overlap(const Matrix& a, const Matrix& b) {
+  if (a.lo() >= b.hi() || b.lo() >= a.hi()) return false;
+  const uint64_t wa = (uint64_t)a.cols * a.size(), wb = (uint64_t)b.cols * b.size();
+  const uint64_t la = (uint64_t)a.ld * a.size(), lb = (uint64_t)b.ld * b.size();
+  const uint64_t pitch = a.rows > 1 ? la : lb;
+  if ((a.rows > 1 && b.rows > 1 && la != lb) || pitch < wa || pitch < wb) return true;
+  const uint64_t apart = b.lo() >= a.lo() ? (b.lo() - a.lo()) % pitch : (pitch - (a.lo() - b.lo()) % pitch) % pitch;
+  return apart < wa || apart + wb > pitch;
+}
+
+// Written matrices against all others; `may_be[i]`: matrix i may be matrix 0 itself.
+int check_overlaps(const Matrix* m, const bool* may_be_first, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (!m[i].written && !m[j].written) continue;
+      if (i == 0 && may_be_first[j] && m[0].is(m[j])) continue;
+      if (overlap(m[i], m[j])) return fail(MUON_EINVAL, "%s overlaps %s", m[i].what, m[j].what);
+    }
+  return MUON_OK;
+}
+
+int check_epilogue(int act, float dropout, const int64_t* rng) {
+  if (act < MUON_ACT_NONE || act > MUON_ACT_RELU2) return fail(MUON_EINVAL, "act = %d is no activation", act);
+  if (!(dropout >= 0.0f && dropout < 1.0f)) return fail(MUON_EINVAL, "dropout = %g outside [0, 1)", (double)dropout);
+  if ((uintptr_t)rng % 8) return fail(MUON_EINVAL, "rng is not 8-byte aligned");
+  return MUON_OK;
+}
+
+void fill_dropout(LinEpilogue* e, float p, uint64_t seed, uint32_t step, uint32_t site, const int64_t* rng) {
+  e->border = std::min((uint32_t)std::floor(65536.0 * (double)p + 0.5), 65535u);
+  e->keep_scale = (float)(65536.0 / (65536.0 - e->border));
+  e->seed = seed;
+  e->step = step;
+  e->site = site;
+  e->rng = rng;
+}
+
+// Whether the kernels can read a matrix in place.
+bool readable(const Matrix& m, int type) {
+  return m.type == type && m.lo() % 16 == 0 && m.cols % 8 == 0 &&
+         (m.rows == 1 || (m.ld % 8 == 0 && m.ld >= m.cols && m.ld <= MAX_WIDTH));
+}
+
+size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+// Takes `bytes` from the workspace.
+char* take(LinPlan* p, void* workspace, size_t bytes) {
+  const uintptr_t at = (uintptr_t)workspace + p->workspace;
+  p->workspace += round_up(bytes, 256);
+  return (char*)at;
+}
+
+// The operand that the kernels read for m, through a copy where they must.
+LinOperand operand_of(const Matrix& m, int type, LinPlan* plan, void* workspace) {
+  if (readable(m, type)) {
+    const int64_t ld = m.rows == 1 ? m.cols : m.ld;
+    return {m.p, ld * 2, ((m.rows - 1) * ld + m.cols) * 2};
+  }
+  const int64_t ld = (m.cols + 7) / 8 * 8;
+  char* dst = take(plan, workspace, (size_t)(m.rows * ld * 2));
+  plan->pack.job[plan->pack.n++] = {m.p, dst, m.ld, ld, m.rows, m.cols, m.type, type};
+  return {dst, ld * 2, m.rows * ld * 2};
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tiles, slices and splits of a product.
+int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
+  LinGemmArgs& g = p->gemm;
+  p->tile = LIN_TILE_128;
+  const LinTileSize t = kLinTile[p->tile];
+  g.m = (int32_t)m;
+  g.n = (int32_t)n;
+  g.k = (int32_t)k;
+  g.slices = ceil_div(k, LIN_BK);
+  const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn;
+  int splits = 1;
+  if (grad) {
+    // a split leaves its sums in memory and a last pass reads them: only as
+    // many as fill the compute units, of at least 8 slices each
+    const int64_t fill = 256 / (tm * tn);
+    splits = (int)std::max<int64_t>(1, std::min<int64_t>(fill, g.slices / 8));
+  }
+  g.per_split = g.slices ? ceil_div(g.slices, splits) : 0;
+  g.splits = g.slices ? ceil_div(g.slices, g.per_split) : 1;
+  // a grid holds fewer than 2^32 threads
+  if (tm * tn * g.splits >= (1 << 22)) return fail(MUON_EINVAL, "a product of %lld x %lld is too large", (long long)m, (long long)n);
+  g.tiles_m = (int32_t)tm;
+  g.tiles_n = (int32_t)tn;
+  return MUON_OK;
+}
+
+// sizes_only: pointers may be anything (the size of the workspace is asked for).
+int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool sizes_only, LinPlan* p) {
+  *p = LinPlan{};
+  int rc;
+  if (!l) return fail(MUON_EINVAL, "arguments are NULL");
+  if ((rc = check_dim(l->m, 0, MAX_ROWS, "m")) || (rc = check_dim(l->k, 1, MAX_WIDTH, "k")) ||
+      (rc = check_dim(l->n, 1, MAX_WIDTH, "n")))
+    return rc;
+  if (l->w_transposed != 0 && l->w_transposed != 1) return fail(MUON_EINVAL, "w_transposed = %d is not 0 or 1", l->w_transposed);
+  if ((rc = check_epilogue(l->act, l->dropout, l->rng))) return rc;
+  const int64_t in = backward ? l->n : l->k, out = backward ? l->k : l->n;  // widths of x and y
+  const int type = l->x_type;
+  if (type != MUON_BF16 && type != MUON_FP16) return fail(MUON_EINVAL, "x_type = %d: the products take MUON_BF16 and MUON_FP16", type);
+  if (l->w_type != type && l->w_type != MUON_FP32) return fail(MUON_EINVAL, "w_type = %d is neither x_type nor MUON_FP32", l->w_type);
+  if (l->y_type != type && l->y_type != MUON_FP32) return fail(MUON_EINVAL, "y_type = %d is neither x_type nor MUON_FP32", l->y_type);
+  if (l->bias && l->bias_type != type && l->bias_type != MUON_FP32)
+    return fail(MUON_EINVAL, "bias_type = %d is neither x_type nor MUON_FP32", l->bias_type);
+  if (backward && l->bias) return fail(MUON_EINVAL, "the gradient of the input takes no bias");
+  if (backward && (l->act != MUON_ACT_NONE) != (l->preact != nullptr))
+    return fail(MUON_EINVAL, "act and preact of the layer below come together");
+  p->type = type;
+  if (l->m == 0) {
+    p->empty = true;
+    return MUON_OK;
+  }
+  const Matrix y = {"y", l->y, l->m, out, l->ldy, l->y_type, true};
+  const Matrix x = {"x", l->x, l->m, in, l->ldx, type, false};
+  const int64_t w_rows = l->w_transposed ? l->n : l->k, w_cols = l->w_transposed ? l->k : l->n;
+  const Matrix w = {"w", l->w, w_rows, w_cols, l->ldw, l->w_type, false};
+  if (!sizes_only) {
+    Matrix all[6] = {y, x, w};
+    bool may_be_y[6] = {};
+    int n = 3;
+    if (l->bias) all[n++] = {"bias", l->bias, 1, out, out, l->bias_type, false};
+    if (l->preact) {
+      may_be_y[n] = backward;
+      all[n++] = {"preact", l->preact, l->m, out, l->ldp, type, !backward};
+    }
+    if (l->residual) {
+      may_be_y[n] = true;
+      all[n++] = {"residual", l->residual, l->m, out, l->ldr, l->y_type, false};
+    }
+    for (int i = 0; i < n; ++i)
+      if ((rc = check_matrix(all[i]))) return rc;
+    if ((rc = check_overlaps(all, may_be_y, n))) return rc;
+    if (l->rng && l->dropout > 0.0f) {
+      const Matrix rng = {"rng", l->rng, 1, 4, 4, MUON_FP32, false};
+      for (int i = 0; i < n; ++i)
+        if (all[i].written && overlap(all[i], rng)) return fail(MUON_EINVAL, "%s overlaps rng", all[i].what);
+    }
+  }
+  if ((rc = lay_out(p, l->m, out, in, false))) return rc;
+  LinGemmArgs& g = p->gemm;
+  g.a = operand_of(x, type, p, workspace);
+  g.b = operand_of(w, type, p, workspace);
+  // the reduced index runs along w's rows where it is the one they run along
+  p->b_kmajor = (l->w_transposed != 0) == backward;
+  LinEpilogue& e = g.e;
+  e.bias = l->bias;
+  e.bias_type = l->bias_type;
+  e.residual = l->residual;
+  e.ldr = l->ldr;
+  e.y = l->y;
+  e.ldy = l->ldy;
+  e.y_type = l->y_type;
+  e.preact = l->preact;
+  e.ldp = l->ldp;
+  e.act = l->act;
+  e.backward = backward;
+  fill_dropout(&e, l->dropout, l->seed, l->step, l->site, l->rng);
+  return MUON_OK;
+}
+
+int plan_grad(const muon_linear_dw_t* l, void* workspace, bool sizes_only, LinPlan* p) {
+  *p = LinPlan{};
+  int rc;
+  if (!l) return fail(MUON_EINVAL, "arguments are NULL");
+  if ((rc = check_dim(l->m, 0, MAX_ROWS, "m")) || (rc = check_dim(l->k, 1, MAX_WIDTH, "k")) ||
+      (rc = check_dim(l->n, 1, MAX_WIDTH, "n")))
+    return rc;
+  if (l->dw_transposed != 0 && l->dw_transposed != 1) return fail(MUON_EINVAL, "dw_transposed = %d is not 0 or 1", l->dw_transposed);
+  if (l->accumulate != 0 && l->accumulate != 1) return fail(MUON_EINVAL, "accumulate = %d is not 0 or 1", l->accumulate);
+  const int type = l->type;
+  if (type != MUON_BF16 && type != MUON_FP16) return fail(MUON_EINVAL, "type = %d: the products take MUON_BF16 and MUON_FP16", type);
+  p->type = type;
+  const int64_t rows = l->dw_transposed ? l->n : l->k, cols = l->dw_transposed ? l->k : l->n;
+  const Matrix dw = {"dw", l->dw, rows, cols, l->lddw, MUON_FP32, true};
+  const Matrix x = {"x", l->x, l->m, l->k, l->ldx, type, false};
+  const Matrix dz = {"dz", l->dz, l->m, l->n, l->lddz, type, false};
+  if (!sizes_only) {
+    Matrix all[4] = {dw};
+    const bool none[4] = {};
+    int n = 1;
+    if (l->dbias) all[n++] = {"dbias", l->dbias, 1, l->n, l->n, MUON_FP32, true};
+    if (l->m > 0) {
+      all[n++] = x;
+      all[n++] = dz;
+    }
+    for (int i = 0; i < n; ++i)
+      if ((rc = check_matrix(all[i]))) return rc;
+    if ((rc = check_overlaps(all, none, n))) return rc;
+  }
+  p->empty = l->m == 0 && l->accumulate;
+  if ((rc = lay_out(p, rows, cols, l->m, true))) return rc;
+  LinGemmArgs& g = p->gemm;
+  if (l->m > 0) {
+    const LinOperand ox = operand_of(x, type, p, workspace), oz = operand_of(dz, type, p, workspace);
+    g.a = l->dw_transposed ? oz : ox;
+    g.b = l->dw_transposed ? ox : oz;
+  }
+  g.c = l->dw;
+  g.ldc = l->lddw;
+  g.add = l->accumulate;
+  g.sums = l->dbias;
+  g.sum_side = !l->dbias ? 0 : l->dw_transposed ? 2 : 1;
+  if (g.splits > 1) {
+    const LinTileSize t = kLinTile[p->tile];
+    LinFinishArgs& f = p->fin;
+    p->finish = true;
+    f.part_ld = (int64_t)g.tiles_n * t.bn;
+    f.part_stride = f.part_ld * g.tiles_m * t.bm;
+    g.part = (float*)take(p, workspace, (size_t)(f.part_stride * g.splits * 4));
+    f.c = g.c;
+    f.ldc = g.ldc;
+    f.add = g.add;
+    f.part = g.part;
+    f.m = g.m;
+    f.n = g.n;
+    f.splits = g.splits;
+    f.sum_first_block = ceil_div((int64_t)g.m * ((g.n + 7) / 8), FINISH_THREADS);
+    if (g.sum_side) {
+      f.sums = g.sums;
+      f.n_sums = (int32_t)l->n;
+      f.sum_rows = g.splits * (g.sum_side == 1 ? g.tiles_m : g.tiles_n);
+      f.sum_stride = g.sum_side == 1 ? f.part_ld : (int64_t)g.tiles_m * t.bm;
+      g.sum_part = (float*)take(p, workspace, (size_t)(f.sum_stride * f.sum_rows * 4));
+      f.sum_part = g.sum_part;
+    }
+  }
+  return MUON_OK;
+}
+
+// The workspace as the caller gave it.
+int check_workspace(const LinPlan& p, const void* workspace, size_t bytes) {
+  if (p.empty || p.workspace == 0) return MUON_OK;
+  int64_t copied = 0;  // blocks of the copies
+  for (int i = 0; i < p.pack.n; ++i) copied += pack_blocks(p.pack.job[i]);
+  if (copied > MAX_LAUNCH_ITEMS) return fail(MUON_EINVAL, "operands that have to be copied are too large");
+  if (!workspace) return fail(MUON_EINVAL, "workspace is NULL; this call needs %zu bytes", p.workspace);
+  if ((uintptr_t)workspace % 16) return fail(MUON_EINVAL, "workspace is not 16-byte aligned");
+  if (bytes < p.workspace) return fail(MUON_ENOMEM, "workspace of %zu bytes; this call needs %zu", bytes, p.workspace);
+  return MUON_OK;
+}
+
+int check_workspace_apart(const LinPlan& p, const void* workspace, const Matrix* m, int n) {
+  if (p.empty || p.workspace == 0) return MUON_OK;
+  const Matrix ws = {"workspace", workspace, 1, (int64_t)(p.workspace / 4), (int64_t)(p.workspace / 4), MUON_FP32, true};
+  for (int i = 0; i < n; ++i)
+    if (m[i].p && m[i].rows > 0 && m[i].lo() < ws.hi() && ws.lo() < m[i].hi())
+      return fail(MUON_EINVAL, "workspace overlaps %s", m[i].what);
+  return MUON_OK;
+}
+
+}  // namespace
+
+int plan_linear(const muon_linear_t* l, bool backward, void* workspace, size_t workspace_bytes, LinPlan* out) {
+  int rc = plan_layer(l, backward, workspace, false, out);
+  if (rc || (rc = check_workspace(*out, workspace, workspace_bytes)) || out->empty) return rc;
+  const int64_t in = backward ? l->n : l->k, to = backward ? l->k : l->n;
+  const Matrix all[] = {{"y", l->y, l->m, to, l->ldy, l->y_type, true},
+                        {"x", l->x, l->m, in, l->ldx, l->x_type, false},
+                        {"w", l->w, l->w_transposed ? l->n : l->k, l->w_transposed ? l->k : l->n, l->ldw, l->w_type, false},
+                        {"bias", l->bias, 1, to, to, l->bias_type, false},
+                        {"preact", l->preact, l->m, to, l->ldp, l->x_type, !backward},
+                        {"residual", l->residual, l->m, to, l->ldr, l->y_type, false},
+                        {"rng", l->rng, 1, 4, 4, MUON_FP32, false}};
+  return check_workspace_apart(*out, workspace, all, 7);
+}
+
+int plan_linear_dw(const muon_linear_dw_t* l, void* workspace, size_t workspace_bytes, LinPlan* out) {
+  int rc = plan_grad(l, workspace, false, out);
+  if (rc || (rc = check_workspace(*out, workspace, workspace_bytes)) || out->empty) return rc;
+  const Matrix all[] = {{"dw", l->dw, l->dw_transposed ? l->n : l->k, l->dw_transposed ? l->k : l->n, l->lddw, MUON_FP32, true},
+                        {"dbias", l->dbias, 1, l->n, l->n, MUON_FP32, true},
+                        {"x", l->x, l->m, l->k, l->ldx, l->type, false},
+                        {"dz", l->dz, l->m, l->n, l->lddz, l->type, false}};
+  return check_workspace_apart(*out, workspace, all, 4);
+}
+
+int linear_workspace(const muon_linear_t* l, bool backward, size_t* bytes) {
+  LinPlan p;
+  const int rc = plan_layer(l, backward, nullptr, true, &p);
+  *bytes = rc ? 0 : p.workspace;
+  return rc;
+}
+
+int linear_dw_workspace(const muon_linear_dw_t* l, size_t* bytes) {
+  LinPlan p;
+  const int rc = plan_grad(l, nullptr, true, &p);
+  *bytes = rc ? 0 : p.workspace;
+  return rc;
+}
+
+int plan_dropout(const muon_dropout_t* d, DropArgs* out, int64_t* blocks) {
+  *out = DropArgs{};
+  *blocks = 0;
+  int rc;
+  if (!d) return fail(MUON_EINVAL, "arguments are NULL");
+  if ((rc = check_dim(d->m, 0, MAX_ROWS, "m")) || (rc = check_dim(d->n, 0, MUON_DROPOUT_MAX_COLS, "n"))) return rc;
+  if ((rc = check_epilogue(d->act, d->dropout, d->rng))) return rc;
+  if ((d->act != MUON_ACT_NONE) != (d->preact != nullptr)) return fail(MUON_EINVAL, "act and preact come together");
+  if (d->x_type < MUON_FP32 || d->x_type > MUON_FP16) return fail(MUON_EINVAL, "x_type = %d is no element type", d->x_type);
+  if (d->y_type < MUON_FP32 || d->y_type > MUON_FP16) return fail(MUON_EINVAL, "y_type = %d is no element type", d->y_type);
+  if (d->m == 0 || d->n == 0) return MUON_OK;
+  Matrix all[4] = {{"y", d->y, d->m, d->n, d->ldy, d->y_type, true}, {"x", d->x, d->m, d->n, d->ldx, d->x_type, false}};
+  const bool may_be_y[4] = {false, true, true, true};
+  int n = 2;
+  if (d->preact) all[n++] = {"preact", d->preact, d->m, d->n, d->ldp, d->x_type, false};
+  if (d->residual) all[n++] = {"residual", d->residual, d->m, d->n, d->ldr, d->y_type, false};
+  for (int i = 0; i < n; ++i)
+    if ((rc = check_matrix(all[i]))) return rc;
+  if ((rc = check_overlaps(all, may_be_y, n))) return rc;
+  if (d->rng && d->dropout > 0.0f && overlap(all[0], Matrix{"rng", d->rng, 1, 4, 4, MUON_FP32, false}))
+    return fail(MUON_EINVAL, "y overlaps rng");
+  const int64_t eights = d->m * ((d->n + 7) / 8), per_block = DROP_THREADS * DROP_CHUNKS;
+  *blocks = (eights + per_block - 1) / per_block;
+  if (*blocks > MAX_LAUNCH_ITEMS) return fail(MUON_EINVAL, "%lld x %lld elements are too many", (long long)d->m, (long long)d->n);
+  out->x = d->x;
+  out->ldx = d->ldx;
+  out->m = d->m;
+  out->n = d->n;
+  out->x_type = d->x_type;
+  LinEpilogue& e = out->e;
+  e.residual = d->residual;
+  e.ldr = d->ldr;
+  e.y = d->y;
+  e.ldy = d->ldy;
+  e.y_type = d->y_type;
+  e.preact = const_cast<void*>(d->preact);
+  e.ldp = d->ldp;
+  e.act = d->act;
+  e.backward = 1;
+  fill_dropout(&e, d->dropout, d->seed, d->step, d->site, d->rng);
+  return MUON_OK;
+}
+
+}  // namespace muon

@@ -1,0 +1,126 @@
+// Kernel arguments and constants of the hidden layers' products and of
+// dropout.  Plain C++ (no HIP headers): shared by the host code that fills
+// them in and the gfx950 kernels that read them.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "grad_types.h"
+
+namespace muon {
+
+enum LinAct { LIN_ACT_NONE = 0, LIN_ACT_GELU = 1, LIN_ACT_RELU = 2, LIN_ACT_RELU2 = 3 };
+
+// The generator: Philox 4x32 (Salmon, Moraes, Dror and Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC'11) with 7 rounds, the fewest that pass
+// their whole test battery.  One call makes the 16 random bits of 8 elements.
+constexpr int DROP_ROUNDS = 7;
+
+// What is done to a product (or to a tensor, by muon_dropout) before it is
+// stored; v is fp32 throughout and rounded once.
+//   forward   z = v + bias;  [preact = z];  y = residual + drop(act(z))
+//   backward  y = residual + drop(v) act'(preact)
+struct LinEpilogue {
+  const void* bias;  // of n elements, or null
+  const void* residual;  // of y's type, or null
+  void* y;
+  void* preact;  // of the product's type; written forward, read backward; or null
+  const int64_t* rng;  // {seed, step} on the device, or null
+  int64_t ldr, ldy, ldp;
+  uint64_t seed;
+  uint32_t step, site;
+  uint32_t border;  // elements whose 16 bits are below it are dropped; 0: no dropout
+  float keep_scale;
+  int32_t bias_type, y_type;
+  int32_t act;
+  int32_t backward;
+};
+
+// An operand as the products read it: 16-bit elements, 16-byte aligned, rows of
+// a multiple of 8 elements apart, rows of a multiple of 8 elements.
+struct LinOperand {
+  const void* p;
+  int64_t ld;     // bytes from row to row
+  int64_t bytes;  // from p to the end of the last row
+};
+
+// Rows copied into such an operand, or rounded to its type.
+struct LinPack {
+  const void* src;
+  void* dst;
+  int64_t src_ld, dst_ld;  // elements; dst_ld is cols rounded up to 8, filled with zeros
+  int64_t rows, cols;
+  int32_t src_type, dst_type;
+};
+struct LinPackArgs {
+  LinPack job[2];
+  int32_t n;
+};
+constexpr int PACK_THREADS = 256, PACK_CHUNKS = 4;  // of 8 elements, per thread
+constexpr int64_t pack_blocks(const LinPack& p) {
+  return (p.rows * ((p.cols + 7) / 8) + PACK_THREADS * PACK_CHUNKS - 1) / (PACK_THREADS * PACK_CHUNKS);
+}
+
+// One product C = A B, m x n over k.  Output tiles are numbered in groups of
+// LIN_GROUP tile rows, column by column within a group, and each XCD takes a run
+// of them: the 32 tiles that its compute units hold at a time then share 8
+// row panels and 4 column panels in its L2.
+constexpr int LIN_BK = 64;  // elements of a K slice
+constexpr int LIN_GROUP = 8;
+struct LinGemmArgs {
+  LinOperand a, b;
+  int32_t m, n, k;
+  int32_t tiles_m, tiles_n;
+  int32_t slices;     // of K
+  int32_t splits;     // of the slices; above 1 every split leaves its sums in part
+  int32_t per_split;  // slices of a split
+  LinEpilogue e;      // of the products of a layer
+  // Of a weight gradient: C to c, or added to it; sums of the rows of dz (the B
+  // operand's columns where sum_side is 1, the A operand's where it is 2) to
+  // sums.  With splits, part holds splits x (tiles_m BM) x (tiles_n BN) sums and
+  // sum_part splits x (the other side's tiles) x (sum_side's tiles x edge).
+  float* c;
+  float* sums;
+  float* part;
+  float* sum_part;
+  int64_t ldc;
+  int32_t add;
+  int32_t sum_side;
+};
+static_assert(sizeof(LinGemmArgs) <= KERNARG_BYTES, "kernel arguments");
+
+// c = [c +] the sums of the splits; likewise sums.
+struct LinFinishArgs {
+  float* c;
+  float* sums;
+  const float* part;
+  const float* sum_part;
+  int64_t ldc;
+  int64_t part_ld, part_stride;          // of part, in elements
+  int64_t sum_stride;                    // of sum_part
+  int32_t m, n, n_sums;
+  int32_t splits, sum_rows;              // rows of sum_part to add
+  int32_t add;
+  int32_t sum_first_block;               // blocks from here on take the sums
+};
+constexpr int FINISH_THREADS = 256;
+
+// Output tiles of the product kernels (see kernels_linear.hip and linear_host.cpp).
+enum LinTile { LIN_TILE_128 = 0, LIN_TILES };
+struct LinTileSize {
+  int bm, bn;
+};
+constexpr LinTileSize kLinTile[LIN_TILES] = {{128, 128}};
+
+// Dropout by itself.
+struct DropArgs {
+  const void* x;
+  int64_t ldx;
+  int64_t m, n;
+  int32_t x_type;
+  LinEpilogue e;  // backward form, preact of x's type
+};
+constexpr int DROP_THREADS = 256, DROP_CHUNKS = 4;  // of 8 elements, per thread
+
+}  // namespace muon

@@ -603,7 +603,7 @@ int muon_set_lanes(int lanes) {
 
 int muon_timing_enable(int kernel) {
   clear_error();
-  if (kernel < -1 || kernel > MUON_KERNEL_GRAD_CLIP) return fail(MUON_EINVAL, "unknown kernel family %d", kernel);
+  if (kernel < -1 || kernel > MUON_KERNEL_DROPOUT) return fail(MUON_EINVAL, "unknown kernel family %d", kernel);
   std::lock_guard<std::mutex> lock(api_mutex());
   g_time_kind = kernel;
   g_ev_used = 0;

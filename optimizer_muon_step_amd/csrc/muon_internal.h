@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "grad_types.h"
+#include "linear_types.h"
 #include "plan_types.h"
 
 namespace muon {
@@ -40,6 +41,15 @@ hipError_t launch_grad_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_grad_small(const GradSmallArgs& a, bool clip, hipStream_t s);
 hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t s);
 hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s);
+
+// A layer's products (type: of the operands; b_kmajor: operand B has rows of the
+// reduced index), the copies and the pass over splits that they may need, and
+// dropout: one launch each.
+hipError_t launch_linear(const LinGemmArgs& a, int type, bool b_kmajor, int tile, hipStream_t s);
+hipError_t launch_linear_dw(const LinGemmArgs& a, int type, int tile, hipStream_t s);
+hipError_t launch_linear_finish(const LinFinishArgs& a, hipStream_t s);
+hipError_t launch_linear_pack(const LinPackArgs& a, hipStream_t s);
+hipError_t launch_dropout(const DropArgs& a, int64_t blocks, hipStream_t s);
 
 // Source and destination of the three arrays (param, exp_avg, exp_avg_sq)
 // of a delayed-untying copy.
