@@ -51,7 +51,7 @@ struct Eights {
 // y = residual + drop(x) act'(preact).  Each thread has all of its loads out
 // before it makes a mask; the last columns of a row that is no multiple of 8
 // long are done one by one.
-template <int XT, int YT>
+template <int XT, int YT, int ACT>
 __global__ __launch_bounds__(DROP_THREADS) void dropout_kernel(const DropArgs a) {
   static_assert(DROP_THREADS * DROP_CHUNKS <= 1024, "see Eights");
   const LinEpilogue& e = a.e;
@@ -67,14 +67,14 @@ __global__ __launch_bounds__(DROP_THREADS) void dropout_kernel(const DropArgs a)
     whole[t] = row[t] < a.m && col[t] + 8 <= a.n;
     if (!whole[t]) continue;
     x[t] = load8<XT>(a.x, row[t] * a.ldx + col[t]);
-    if (e.act != LIN_ACT_NONE) z[t] = load8<XT>(e.preact, row[t] * e.ldp + col[t]);
+    if constexpr (ACT != LIN_ACT_NONE) z[t] = load8<XT>(e.preact, row[t] * e.ldp + col[t]);
     if (e.residual) r[t] = load8<YT>(e.residual, row[t] * e.ldr + col[t]);
   }
 #pragma unroll
   for (int t = 0; t < DROP_CHUNKS; ++t) {
     if (whole[t]) {
       f32x8 v = x[t];
-      if (e.act != LIN_ACT_NONE) v = slope8(z[t], e.act) * v;
+      if constexpr (ACT != LIN_ACT_NONE) v = slope8<ACT>(z[t]) * v;
       if (e.border != 0) v = drop8(e, key, row[t], col[t], v);
       if (e.residual) v = r[t] + v;
       store8<YT>(e.y, row[t] * e.ldy + col[t], v);
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(DROP_THREADS) void dropout_kernel(const DropArgs a)
 #pragma unroll 1
       for (int64_t c = col[t]; c < a.n; ++c) {
         float v = load1<XT>(a.x, row[t] * a.ldx + c);
-        if (e.act != LIN_ACT_NONE) v *= act_slope(load1<XT>(e.preact, row[t] * e.ldp + c), e.act);
+        if constexpr (ACT != LIN_ACT_NONE) v *= act_slope<ACT>(load1<XT>(e.preact, row[t] * e.ldp + c));
         if (e.border != 0) v = drop1(e, key, row[t], c, v);
         if (e.residual) v = load1<YT>(e.residual, row[t] * e.ldr + c) + v;
         store1<YT>(e.y, row[t] * e.ldy + c, v);
@@ -91,17 +91,26 @@ __global__ __launch_bounds__(DROP_THREADS) void dropout_kernel(const DropArgs a)
   }
 }
 
-template <int XT>
+template <int XT, int YT>
 static hipError_t launch_dropout_of(const DropArgs& a, int grid, hipStream_t s) {
-  if (a.e.y_type == GRAD_FP32) dropout_kernel<XT, GRAD_FP32><<<grid, DROP_THREADS, 0, s>>>(a);
-  else if (a.e.y_type == GRAD_BF16) dropout_kernel<XT, GRAD_BF16><<<grid, DROP_THREADS, 0, s>>>(a);
-  else dropout_kernel<XT, GRAD_FP16><<<grid, DROP_THREADS, 0, s>>>(a);
+  switch (a.e.act) {
+    case LIN_ACT_NONE: dropout_kernel<XT, YT, LIN_ACT_NONE><<<grid, DROP_THREADS, 0, s>>>(a); break;
+    case LIN_ACT_GELU: dropout_kernel<XT, YT, LIN_ACT_GELU><<<grid, DROP_THREADS, 0, s>>>(a); break;
+    case LIN_ACT_RELU: dropout_kernel<XT, YT, LIN_ACT_RELU><<<grid, DROP_THREADS, 0, s>>>(a); break;
+    default: dropout_kernel<XT, YT, LIN_ACT_RELU2><<<grid, DROP_THREADS, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
+template <int XT>
+static hipError_t launch_dropout_from(const DropArgs& a, int grid, hipStream_t s) {
+  if (a.e.y_type == GRAD_FP32) return launch_dropout_of<XT, GRAD_FP32>(a, grid, s);
+  return a.e.y_type == GRAD_BF16 ? launch_dropout_of<XT, GRAD_BF16>(a, grid, s) : launch_dropout_of<XT, GRAD_FP16>(a, grid, s);
+}
+
 hipError_t launch_dropout(const DropArgs& a, int64_t blocks, hipStream_t s) {
-  if (a.x_type == GRAD_FP32) return launch_dropout_of<GRAD_FP32>(a, (int)blocks, s);
-  return a.x_type == GRAD_BF16 ? launch_dropout_of<GRAD_BF16>(a, (int)blocks, s) : launch_dropout_of<GRAD_FP16>(a, (int)blocks, s);
+  if (a.x_type == GRAD_FP32) return launch_dropout_from<GRAD_FP32>(a, (int)blocks, s);
+  return a.x_type == GRAD_BF16 ? launch_dropout_from<GRAD_BF16>(a, (int)blocks, s) : launch_dropout_from<GRAD_FP16>(a, (int)blocks, s);
 }
 
 // Operands copied to rows that are aligned and a multiple of 8 long, with

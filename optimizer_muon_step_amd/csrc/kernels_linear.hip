@@ -8,13 +8,14 @@ namespace muon {
 
 using namespace lin;
 
-template <int TYPE, bool BK>
+template <int TYPE, bool BKM>
 static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
-  const int grid = a.tiles_m * a.tiles_n * a.splits;
-  switch (tile) {
-    case LIN_TILE_128:
-      linear_gemm_kernel<TYPE, false, BK, false, 128, 128, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a);
-      break;
+  const int grid = a.tiles_m * a.tiles_n, threads = kLinTile[tile].threads;
+  switch (tile) {  // tile, K slice, waves along m, n and k, stages, blocks to a compute unit
+    case LIN_TILE_256: linear_gemm_kernel<TYPE, false, BKM, false, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_128: linear_gemm_kernel<TYPE, false, BKM, false, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_64: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 64, 2, 2, 2, 5, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_32: linear_gemm_kernel<TYPE, false, BKM, false, 32, 64, 64, 1, 2, 2, 6, 2><<<grid, threads, 0, s>>>(a); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -11,11 +11,11 @@ using namespace lin;
 
 template <int TYPE>
 static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
-  const int grid = a.tiles_m * a.tiles_n * a.splits;
-  switch (tile) {
-    case LIN_TILE_128:
-      linear_gemm_kernel<TYPE, true, true, true, 128, 128, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a);
-      break;
+  const int grid = a.tiles_m * a.tiles_n * a.splits, threads = kLinTile[tile].threads;
+  switch (tile) {  // as in kernels_linear.hip
+    case LIN_TILE_256: linear_gemm_kernel<TYPE, true, true, true, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_128: linear_gemm_kernel<TYPE, true, true, true, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_64: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 64, 2, 2, 2, 5, 2><<<grid, threads, 0, s>>>(a); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const Lin
   for (int s = 1; s < a.splits; ++s) v += load8<GRAD_FP32>(a.part + s * a.part_stride, row * a.part_ld + col);
   const GradStore store = {a.c, a.ldc, a.add != 0};
   if (have == 8) {
-    store(row, col, v);
+    store(row, col, v, 0.0f, store.fetch(row, col));
   } else {
 #pragma unroll
     for (int k = 0; k < 7; ++k)

@@ -43,6 +43,13 @@ __device__ __forceinline__ u32x4 narrow8(f32x8 v) {
   }
 }
 
+// 16 bytes of p from element i on.
+template <int TYPE>
+__device__ __forceinline__ u32x4 load_raw(const void* p, int64_t i) {
+  const u32x4_u w = *reinterpret_cast<const MUON_GLOBAL u32x4_u*>(gptr(static_cast<const typename grad::Elem<TYPE>::scalar*>(p)) + i);
+  return u32x4{w.x, w.y, w.z, w.w};
+}
+
 // Elements i .. i + 7 of p, or element i.
 template <int TYPE>
 __device__ __forceinline__ f32x8 load8(const void* p, int64_t i) {
@@ -60,15 +67,24 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
   return grad::Elem<TYPE>::widen1(gptr(static_cast<const typename grad::Elem<TYPE>::scalar*>(p))[i]);
 }
 
+// stream: past the caches.
 template <int TYPE>
-__device__ __forceinline__ void store8(void* p, int64_t i, f32x8 v) {
+__device__ __forceinline__ void store8(void* p, int64_t i, f32x8 v, bool stream = false) {
   MUON_GLOBAL typename grad::Elem<TYPE>::scalar* s = gptr(static_cast<typename grad::Elem<TYPE>::scalar*>(p)) + i;
   if constexpr (TYPE == GRAD_FP32) {
-    *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s) = f32x4_u{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s + 4) = f32x4_u{v[4], v[5], v[6], v[7]};
+    const f32x4_u lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    if (stream) {
+      __builtin_nontemporal_store(lo, reinterpret_cast<MUON_GLOBAL f32x4_u*>(s));
+      __builtin_nontemporal_store(hi, reinterpret_cast<MUON_GLOBAL f32x4_u*>(s + 4));
+    } else {
+      *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s) = lo;
+      *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s + 4) = hi;
+    }
   } else {
     const u32x4 w = narrow8<TYPE>(v);
-    *reinterpret_cast<MUON_GLOBAL u32x4_u*>(s) = u32x4_u{w.x, w.y, w.z, w.w};
+    const u32x4_u u = {w.x, w.y, w.z, w.w};
+    if (stream) __builtin_nontemporal_store(u, reinterpret_cast<MUON_GLOBAL u32x4_u*>(s));
+    else *reinterpret_cast<MUON_GLOBAL u32x4_u*>(s) = u;
   }
 }
 template <int TYPE>
@@ -83,38 +99,53 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
 // the quotient is then -0.
 constexpr float GELU_C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float GELU_C3 = 0.044715f;
-__device__ __forceinline__ float gelu_gate(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __expf(-GELU_C * (z + GELU_C3 * z * z * z)));
+constexpr float LOG2_E = 1.4426950408889634f;
+__device__ __forceinline__ float gelu_exp(float z) {
+  // exp(-2u) = 2^(z (c + c' z^2))
+  return __builtin_amdgcn_exp2f(z * __builtin_fmaf(z * z, -GELU_C * GELU_C3 * LOG2_E, -GELU_C * LOG2_E));
 }
 // A comparison that is false for a NaN keeps it.
-__device__ __forceinline__ float act_of(float z, int act) {
-  if (act == LIN_ACT_GELU) return z * gelu_gate(z);
-  if (act == LIN_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if (act == LIN_ACT_RELU2) return z < 0.0f ? 0.0f : z * z;
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (ACT == LIN_ACT_GELU) return z * __builtin_amdgcn_rcpf(1.0f + gelu_exp(z));
+  if constexpr (ACT == LIN_ACT_RELU) return z < 0.0f ? 0.0f : z;
+  if constexpr (ACT == LIN_ACT_RELU2) return z < 0.0f ? 0.0f : z * z;
   return z;
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == LIN_ACT_GELU) {
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == LIN_ACT_GELU) {
     // s + z s (1 - s) 2u' with 1 - s = exp(-2u) s, which does not cancel.  Beyond
     // 10 the slope is within 1e-34 of 0 or 1, and exp or z^3 may overflow.
-    if (z > 10.0f) return 1.0f;
-    if (z < -10.0f) return 0.0f;
-    const float t = __expf(-GELU_C * (z + GELU_C3 * z * z * z)), s = __builtin_amdgcn_rcpf(1.0f + t);
-    return s + z * s * (t * s) * (GELU_C * (1.0f + 3.0f * GELU_C3 * z * z));
+    const float t = gelu_exp(z), s = __builtin_amdgcn_rcpf(1.0f + t);
+    const float v = __builtin_fmaf(z * s * (t * s), __builtin_fmaf(z * z, 3.0f * GELU_C3 * GELU_C, GELU_C), s);
+    return z > 10.0f ? 1.0f : z < -10.0f ? 0.0f : v;
   }
-  if (act == LIN_ACT_RELU) return z <= 0.0f ? 0.0f : (z > 0.0f ? 1.0f : z);
-  if (act == LIN_ACT_RELU2) return z < 0.0f ? 0.0f : 2.0f * z;
+  if constexpr (ACT == LIN_ACT_RELU) return z <= 0.0f ? 0.0f : (z > 0.0f ? 1.0f : z);
+  if constexpr (ACT == LIN_ACT_RELU2) return z < 0.0f ? 0.0f : 2.0f * z;
   return 1.0f;
 }
-
-__device__ __forceinline__ f32x8 act8(f32x8 v, int act) {
+// By an activation known at run time (uniform over the launch).
+__device__ __forceinline__ float act_of(float z, int act) {
+  if (act == LIN_ACT_GELU) return act_of<LIN_ACT_GELU>(z);
+  if (act == LIN_ACT_RELU) return act_of<LIN_ACT_RELU>(z);
+  return act == LIN_ACT_RELU2 ? act_of<LIN_ACT_RELU2>(z) : z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == LIN_ACT_GELU) return act_slope<LIN_ACT_GELU>(z);
+  if (act == LIN_ACT_RELU) return act_slope<LIN_ACT_RELU>(z);
+  return act == LIN_ACT_RELU2 ? act_slope<LIN_ACT_RELU2>(z) : 1.0f;
+}
+template <int ACT>
+__device__ __forceinline__ f32x8 act8(f32x8 v) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = act_of(v[k], act);
+  for (int k = 0; k < 8; ++k) v[k] = act_of<ACT>(v[k]);
   return v;
 }
-__device__ __forceinline__ f32x8 slope8(f32x8 z, int act) {
+template <int ACT>
+__device__ __forceinline__ f32x8 slope8(f32x8 z) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) z[k] = act_slope(z[k], act);
+  for (int k = 0; k < 8; ++k) z[k] = act_slope<ACT>(z[k]);
   return z;
 }
 

@@ -10,8 +10,11 @@
 // transposed in memory: k-major slices go through the transposing LDS read.
 //
 // Pipeline: WM x WN x WK waves over a BM x BN tile.  K advances in slices of
-// 64 through a ring of NSTAGE LDS buffers that buffer loads fill directly (no
-// registers), every row segment a whole 128-byte line.  Buffer loads bound every access by the
+// BK through a ring of NSTAGE LDS buffers that buffer loads fill directly (no
+// registers), every row segment a whole 128-byte line.  The fragments of a k-step
+// are read while the matrix cores work on the step before, across the slices'
+// borders too: the barrier that hands over the next slice stands before the last
+// k-step of the current one.  Buffer loads bound every access by the
 // operand's own end and give zeros behind it, which serves the rows and
 // columns that a tile hangs over and the rows behind K; the chunks behind K
 // of k-contiguous rows, where the next row follows, get an offset that is
@@ -23,6 +26,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "linear_epilogue.h"
 
@@ -46,13 +51,12 @@ __device__ __forceinline__ void wait_loads() {
 // At most `after` slices of PER loads each, `after` below NSTAGE - 1.
 template <int PER, int NSTAGE>
 __device__ __forceinline__ void wait_slices(int after) {
-  if (NSTAGE > 7 && after >= 6) wait_loads<6 * PER>();
-  else if (NSTAGE > 6 && after == 5) wait_loads<5 * PER>();
-  else if (NSTAGE > 5 && after == 4) wait_loads<4 * PER>();
-  else if (NSTAGE > 4 && after == 3) wait_loads<3 * PER>();
-  else if (NSTAGE > 3 && after == 2) wait_loads<2 * PER>();
-  else if (NSTAGE > 2 && after == 1) wait_loads<PER>();
-  else wait_loads<0>();
+  if constexpr (NSTAGE > 2) {
+    if (after == NSTAGE - 2) wait_loads<(NSTAGE - 2) * PER>();
+    else wait_slices<PER, NSTAGE - 1>(after);
+  } else {
+    wait_loads<0>();
+  }
 }
 
 __device__ __forceinline__ void block_barrier() {
@@ -74,32 +78,33 @@ __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t to, uint32_t of
 }
 
 template <int TYPE>
-__device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
   if constexpr (TYPE == GRAD_BF16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// One operand's slice in LDS: R rows (k-contiguous, 128 bytes each) or 64
-// rows of R elements (k-major), the loads that fill it and the fragment reads.
-template <bool KMAJOR, int R, int NW>
+// One operand's slice in LDS: R rows of BK elements (k-contiguous) or BK rows
+// of R elements (k-major), the loads that fill it and the fragment reads.
+template <bool KMAJOR, int R, int NW, int BK>
 struct Slice {
-  static constexpr int BYTES = R * LIN_BK * 2;
-  static constexpr int LOADS = R / 8 / NW;   // 1 KB each, per wave
-  static constexpr int CHUNKS = KMAJOR ? R / 8 : LIN_BK / 8;  // 16-byte chunks of a row
-  static constexpr int ROWS = 64 / CHUNKS;   // rows of one load
-  static_assert(R % 32 == 0 && LOADS >= 1 && LOADS * 8 * NW == R, "tile does not split into whole loads");
-  static_assert(!KMAJOR || R == 64 || R == 128 || R == 256, "k-major rows of 128, 256 or 512 bytes");
+  static constexpr int BYTES = R * BK * 2;
+  static constexpr int LOADS = BYTES / 1024 / NW;   // 1 KB each, per wave
+  static constexpr int PITCH = KMAJOR ? R * 2 : BK * 2;  // bytes of a row
+  static constexpr int CHUNKS = PITCH / 16;  // 16-byte chunks of a row
+  static_assert(R % 32 == 0 && LOADS >= 1 && LOADS * 1024 * NW == BYTES, "tile does not split into whole loads");
+  static_assert(BK == 64 || BK == 32, "k-contiguous rows of 128 or 64 bytes");
+  static_assert(!KMAJOR || R == 64 || R == 128 || R == 192 || R == 256, "k-major rows of 128, 256, 384 or 512 bytes");
 
   // Chunk swizzle.  A k-contiguous fragment has 16 lanes on 16 rows at
-  // one chunk; two rows share a 256-byte line of the banks, so XOR by (row / 2) % 8
-  // puts the 16 reads on 16 chunks.  A transposing read has each 16 lanes on 4
+  // one chunk; two rows of 64 elements (four of 32) share a 256-byte line of the banks,
+  // so XOR by (row / 2) % 8 ((row / 4) % 4) puts the 16 reads on 16 chunks.  A transposing read has each 16 lanes on 4
   // rows, 32 bytes each, and pairs of such groups 32 bytes apart; the XOR sends the
   // 4 rows to different 64-byte groups of the banks.
   static __device__ __forceinline__ int swz(int row, int chunk) {
-    if (!KMAJOR) return chunk ^ ((row >> 1) & 7);
-    return CHUNKS == 8 ? chunk ^ (4 * ((row >> 1) & 1)) : chunk ^ (4 * (row & 3));
+    if (!KMAJOR) return BK == 64 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
+    return chunk ^ (PITCH % 256 != 0 ? 4 * ((row >> 1) & 1) : 4 * (row & 3)) ^ (2 * ((row >> 3) & 1));
   }
 
   uint64_t base;     // of the slice that is loaded next
@@ -109,14 +114,14 @@ struct Slice {
 
   // Of the tile that starts at row / column `first`, from slice s0 on.
   __device__ __forceinline__ void start(const LinOperand& o, int first, int s0, int wave, int lane) {
-    step = KMAJOR ? LIN_BK * o.ld : LIN_BK * 2;
+    step = KMAJOR ? BK * o.ld : BK * 2;
     const int64_t at = (KMAJOR ? (int64_t)first * 2 : (int64_t)first * o.ld) + s0 * step;
     base = (uint64_t)o.p + at;
     left = o.bytes - at;
 #pragma unroll
     for (int t = 0; t < LOADS; ++t) {
-      const int row = (t * NW + wave) * ROWS + lane / CHUNKS;
-      vo[t] = (uint32_t)(row * (int)o.ld) + swz(row, lane % CHUNKS) * 16;
+      const int slot = (t * NW + wave) * 64 + lane, row = slot / CHUNKS;
+      vo[t] = (uint32_t)(row * (int)o.ld) + swz(row, slot % CHUNKS) * 16;
     }
   }
 
@@ -128,9 +133,9 @@ struct Slice {
 #pragma unroll
     for (int t = 0; t < LOADS; ++t) {
       uint32_t off = vo[t];
-      if (!KMAJOR && have < LIN_BK) {  // have is a multiple of 8
-        const int row = (t * NW + wave) * ROWS + lane / CHUNKS;
-        if (swz(row, lane % CHUNKS) * 8 >= have) off = 0x80000000u;
+      if (!KMAJOR && have < BK) {  // have is a multiple of 8
+        const int slot = (t * NW + wave) * 64 + lane;
+        if (swz(slot / CHUNKS, slot % CHUNKS) * 8 >= have) off = 0x80000000u;
       }
       load_to_lds(rsrc, (uint32_t)(uintptr_t)(to + (t * NW + wave) * 1024), off, t == 0);
     }
@@ -138,29 +143,29 @@ struct Slice {
     left -= step;
   }
 
-  // Offsets within the slice of this lane's reads of the 32 x 16 fragment at
+  // Offsets within the slice of this lane's reads of the 16 x 32 fragment at
   // row / column r0, k-step 0.
   struct Read {
     int lo, hi;
   };
   static __device__ __forceinline__ Read read_of(int r0, int lane) {
+    const int g = lane >> 4, l = lane & 15;
     if (!KMAJOR) {
-      const int r = r0 + (lane & 31);
-      return {r * 128 + swz(r, lane >> 5) * 16, 0};
+      const int r = r0 + l;
+      return {r * PITCH + swz(r, g) * 16, 0};
     }
     // ds_read_b64_tr_b16 transposes 16-bit elements across 16 lanes: with lane L
     // of a group addressing row k0 + L/4, columns j0 + 4(L%4) .. +3, lane i
     // receives column j0 + i of rows k0 .. k0+3
-    const int g = lane >> 4, l = lane & 15;
-    const int k = 8 * (g >> 1) + (l >> 2), j = r0 + 16 * (g & 1) + 4 * (l & 3);
-    return {k * (2 * R) + swz(k, j >> 3) * 16 + (j & 7) * 2, (k + 4) * (2 * R) + swz(k + 4, j >> 3) * 16 + (j & 7) * 2};
+    const int k = 8 * g + (l >> 2), j = r0 + 4 * (l & 3);
+    return {k * PITCH + swz(k, j >> 3) * 16 + (j & 7) * 2, (k + 4) * PITCH + swz(k + 4, j >> 3) * 16 + (j & 7) * 2};
   }
-  // Element i of a lane: row / column r0 + lane % 32, k = 16 kk + 8 (lane / 32) + i.
+  // Element i of a lane: row / column r0 + lane % 16, k = 32 kk + 8 (lane / 16) + i.
   static __device__ __forceinline__ s16x8 fragment(const LIN_LDS char* st, Read r, int kk) {
-    if (!KMAJOR) return *(const LIN_LDS s16x8*)(st + (r.lo ^ (32 * kk)));  // chunk 2 kk further on: an XOR too
-    // 16 rows on: the swizzle is the same
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LIN_LDS s16x4*)(st + r.lo + kk * 16 * (2 * R)));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LIN_LDS s16x4*)(st + r.hi + kk * 16 * (2 * R)));
+    if (!KMAJOR) return *(const LIN_LDS s16x8*)(st + (r.lo ^ (64 * kk)));  // chunk 4 kk further on: an XOR too
+    // 32 rows on: the swizzle is the same
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LIN_LDS s16x4*)(st + r.lo + kk * 32 * PITCH));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LIN_LDS s16x4*)(st + r.hi + kk * 32 * PITCH));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
@@ -171,44 +176,60 @@ __device__ __forceinline__ float fragment_sum(s16x8 f) {
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
-// What a tile's sums become: eight of them at (row, col ..), or one.
-template <int TYPE>
+// What a tile's sums become: eight of them at (row, col ..), or one.  What an eight
+// needs from memory is fetched ahead of it.  ACT and BACKWARD are the launch's.
+template <int TYPE, int ACT, bool BACKWARD>
 struct LayerStore {
   const LinEpilogue& e;
   const DropKey key;
-  __device__ __forceinline__ explicit LayerStore(const LinGemmArgs& a) : e(a.e), key(a.e) {}
+  const bool wide;  // y and the residual are fp32
+  struct Fetched {
+    u32x4 z, r;  // r: of a 16-bit residual; an fp32 one is read where it is added, registers being short
+  };
+  __device__ __forceinline__ LayerStore(const LinEpilogue& e_, const DropKey& k) : e(e_), key(k), wide(e_.y_type == GRAD_FP32) {}
 
-  static __device__ __forceinline__ f32x8 get(int type, const void* p, int64_t i) {
-    return type == GRAD_FP32 ? load8<GRAD_FP32>(p, i) : load8<TYPE>(p, i);
+  __device__ __forceinline__ Fetched fetch(int64_t row, int col) const {
+    Fetched f;
+    if constexpr (BACKWARD && ACT != LIN_ACT_NONE) f.z = load_raw<TYPE>(e.preact, row * e.ldp + col);
+    if (e.residual && !wide) f.r = load_raw<TYPE>(e.residual, row * e.ldr + col);
+    return f;
+  }
+  // bias: of columns col .. col + 7, zeros where there is none
+  __device__ __forceinline__ f32x8 bias(int col) const {
+    if (BACKWARD || !e.bias) return 0.0f;
+    return e.bias_type == GRAD_FP32 ? load8<GRAD_FP32>(e.bias, col) : load8<TYPE>(e.bias, col);
+  }
+  __device__ __forceinline__ void operator()(int64_t row, int col, f32x8 v, f32x8 bias, const Fetched& f) const {
+    if constexpr (!BACKWARD) {
+      v += bias;
+      if (e.preact) store8<TYPE>(e.preact, row * e.ldp + col, v, e.stream);
+      v = act8<ACT>(v);
+    } else if constexpr (ACT != LIN_ACT_NONE) {
+      v = slope8<ACT>(widen8<TYPE>(f.z)) * v;
+    }
+    if (e.border != 0) v = drop8(e, key, row, col, v);
+    if (wide) {
+      if (e.residual) v = load8<GRAD_FP32>(e.residual, row * e.ldr + col) + v;
+      store8<GRAD_FP32>(e.y, row * e.ldy + col, v, e.stream);
+    } else {
+      if (e.residual) v = widen8<TYPE>(f.r) + v;
+      store8<TYPE>(e.y, row * e.ldy + col, v, e.stream);
+    }
   }
   static __device__ __forceinline__ float get1(int type, const void* p, int64_t i) {
     return type == GRAD_FP32 ? load1<GRAD_FP32>(p, i) : load1<TYPE>(p, i);
   }
-
-  __device__ __forceinline__ void operator()(int64_t row, int col, f32x8 v) const {
-    if (!e.backward) {
-      if (e.bias) v += get(e.bias_type, e.bias, col);
-      if (e.preact) store8<TYPE>(e.preact, row * e.ldp + col, v);
-      if (e.act != LIN_ACT_NONE) v = act8(v, e.act);
-    } else if (e.act != LIN_ACT_NONE) {
-      v = slope8(load8<TYPE>(e.preact, row * e.ldp + col), e.act) * v;
-    }
-    if (e.border != 0) v = drop8(e, key, row, col, v);
-    if (e.residual) v = get(e.y_type, e.residual, row * e.ldr + col) + v;
-    if (e.y_type == GRAD_FP32) store8<GRAD_FP32>(e.y, row * e.ldy + col, v);
-    else store8<TYPE>(e.y, row * e.ldy + col, v);
-  }
   __device__ __forceinline__ void one(int64_t row, int col, float v) const {
-    if (!e.backward) {
+    if constexpr (!BACKWARD) {
       if (e.bias) v += get1(e.bias_type, e.bias, col);
       if (e.preact) store1<TYPE>(e.preact, row * e.ldp + col, v);
-      v = act_of(v, e.act);
-    } else if (e.act != LIN_ACT_NONE) {
-      v *= act_slope(load1<TYPE>(e.preact, row * e.ldp + col), e.act);
+      v = act_of<ACT>(v);
+    } else if constexpr (ACT != LIN_ACT_NONE) {
+      v *= act_slope<ACT>(load1<TYPE>(e.preact, row * e.ldp + col));
     }
     if (e.border != 0) v = drop1(e, key, row, col, v);
     if (e.residual) v = get1(e.y_type, e.residual, row * e.ldr + col) + v;
-    if (e.y_type == GRAD_FP32) store1<GRAD_FP32>(e.y, row * e.ldy + col, v);
+    if (wide) store1<GRAD_FP32>(e.y, row * e.ldy + col, v);
     else store1<TYPE>(e.y, row * e.ldy + col, v);
   }
 };
@@ -217,9 +238,17 @@ struct GradStore {
   float* c;
   int64_t ldc;
   bool add;
-  __device__ __forceinline__ void operator()(int64_t row, int col, f32x8 v) const {
-    if (add) v = load8<GRAD_FP32>(c, row * ldc + col) + v;
-    store8<GRAD_FP32>(c, row * ldc + col, v);
+  struct Fetched {
+    f32x8 c;
+  };
+  __device__ __forceinline__ Fetched fetch(int64_t row, int col) const {
+    Fetched f;
+    if (add) f.c = load8<GRAD_FP32>(c, row * ldc + col);
+    return f;
+  }
+  __device__ __forceinline__ f32x8 bias(int) const { return 0.0f; }
+  __device__ __forceinline__ void operator()(int64_t row, int col, f32x8 v, f32x8, const Fetched& f) const {
+    store8<GRAD_FP32>(c, row * ldc + col, add ? f.c + v : v);
   }
   __device__ __forceinline__ void one(int64_t row, int col, float v) const {
     if (add) v = load1<GRAD_FP32>(c, row * ldc + col) + v;
@@ -227,21 +256,24 @@ struct GradStore {
   }
 };
 
-template <int TYPE, bool AK, bool BK, bool GRAD, int BM, int BN, int WM, int WN, int WK, int NSTAGE>
-__global__ __launch_bounds__(64 * WM * WN * WK) void linear_gemm_kernel(const LinGemmArgs a) {
+// BLOCKS: blocks a compute unit is to hold.
+template <int TYPE, bool AK, bool BKM, bool GRAD, int BM, int BN, int BK, int WM, int WN, int WK, int NSTAGE, int BLOCKS>
+__global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void linear_gemm_kernel(const LinGemmArgs a) {
   constexpr int NW = WM * WN * WK;
   constexpr int WTM = BM / WM, WTN = BN / WN;  // wave tile
-  constexpr int TM = WTM / 32, TN = WTN / 32;
-  typedef Slice<AK, BM, NW> SA;
-  typedef Slice<BK, BN, NW> SB;
+  constexpr int TM = WTM / 16, TN = WTN / 16, PARTS = WTM / 32;
+  typedef Slice<AK, BM, NW, BK> SA;
+  typedef Slice<BKM, BN, NW, BK> SB;
   constexpr int STAGE = SA::BYTES + SB::BYTES;
   constexpr int PER = SA::LOADS + SB::LOADS;
-  constexpr int STEPS = LIN_BK / 16;
+  constexpr int STEPS = BK / 32 / WK;  // k-steps of a wave in a slice
   constexpr int PITCH = WTN * 4 + 16;  // staged fp32 rows: 16 bytes more move each row to other banks
-  constexpr int STAGED = NW * 32 * PITCH;
+  constexpr int AHEAD = PARTS > 1 && NW * 64 * PITCH <= 160 * 1024 / BLOCKS ? 2 : 1;  // 32-row parts of a wave tile staged at once
+  constexpr int STAGED = NW * AHEAD * 32 * PITCH;
   constexpr int LDS = NSTAGE * STAGE > STAGED ? NSTAGE * STAGE : STAGED;
-  static_assert(NSTAGE >= 2 && NSTAGE <= 8 && (NSTAGE - 2) * PER < 64 && LDS <= 160 * 1024, "ring");
-  static_assert(STEPS % WK == 0 && TM * 32 == WTM && TN * 32 == WTN, "wave tile");
+  static_assert(NSTAGE >= 2 && NSTAGE <= 8 && (NSTAGE - 1) * PER < 64 && LDS <= 160 * 1024, "ring");
+  static_assert(STEPS >= 1 && STEPS * WK * 32 == BK && PARTS * 32 == WTM && TN * 16 == WTN, "wave tile");
+  static_assert(STEPS % 2 == 0 || STEPS == 1, "the two sets of fragments change places within a slice");
   __shared__ __attribute__((aligned(16))) char lds[LDS];
 
   const int lane = threadIdx.x & 63;
@@ -265,19 +297,22 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void linear_gemm_kernel(const Li
   lb.start(a.b, col0, s0, wave, lane);
   auto stage_of = [&](int s) { return (LIN_LDS char*)lds + (s % NSTAGE) * STAGE; };
   auto issue = [&](int s) {
-    const int have = a.k - (s0 + s) * LIN_BK;
+    const int have = a.k - (s0 + s) * BK;
     la.load(stage_of(s), have, wave, lane);
     lb.load(stage_of(s) + SA::BYTES, have, wave, lane);
   };
+#pragma unroll
+  for (int s = 0; s < NSTAGE; ++s)
+    if (s < slices) issue(s);
 
   typename SA::Read ra[TM];
   typename SB::Read rb[TN];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) ra[i] = SA::read_of(wi * WTM + i * 32, lane);
+  for (int i = 0; i < TM; ++i) ra[i] = SA::read_of(wi * WTM + i * 16, lane);
 #pragma unroll
-  for (int j = 0; j < TN; ++j) rb[j] = SB::read_of(wj * WTN + j * 32, lane);
+  for (int j = 0; j < TN; ++j) rb[j] = SB::read_of(wj * WTN + j * 16, lane);
 
-  f32x16 acc[TM][TN];
+  f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -290,113 +325,190 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void linear_gemm_kernel(const Li
   const int sharers = GRAD && a.splits > 1 ? (a.sum_side == 1 ? a.tiles_m : a.tiles_n) : 1;
   const bool summing = GRAD && ((a.sum_side == 1 && wi == 0) || (a.sum_side == 2 && wj == 0)) && (a.splits > 1 || across == 0);
 
-  auto compute = [&](int s) {
+  s16x8 fa[2][TM], fb[2][TN];
+  auto read = [&](int s, int step, int set) {
     const LIN_LDS char* sa = stage_of(s);
-    const LIN_LDS char* sb = sa + SA::BYTES;
+    const int kk = WK == 1 ? step : step * WK + wk;
 #pragma unroll
-    for (int t = 0; t < STEPS / WK; ++t) {
-      const int kk = WK == 1 ? t : t * WK + wk;
-      s16x8 fa[TM], fb[TN];
+    for (int i = 0; i < TM; ++i) fa[set][i] = SA::fragment(sa, ra[i], kk);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = SA::fragment(sa, ra[i], kk);
+    for (int j = 0; j < TN; ++j) fb[set][j] = SB::fragment(sa + SA::BYTES, rb[j], kk);
+  };
+  auto multiply = [&](int set) {
+    // operands swapped: a lane then holds 4 consecutive columns of one row
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = SB::fragment(sb, rb[j], kk);
-      // operands swapped: a lane then holds 4 consecutive columns of one row
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<TYPE>(fb[j], fa[i], acc[i][j]);
-    }
-    if constexpr (GRAD) {
-      if (summing && (sharers == 1 || (s0 + s) % sharers == across)) {
-#pragma unroll
-        for (int t = 0; t < STEPS / WK; ++t) {
-          const int kk = WK == 1 ? t : t * WK + wk;
-          if (a.sum_side == 1) {
-#pragma unroll
-            for (int j = 0; j < TN; ++j) sum[j] += fragment_sum<TYPE>(SB::fragment(sb, rb[j], kk));
-          } else {
-#pragma unroll
-            for (int i = 0; i < TM; ++i) sum[i] += fragment_sum<TYPE>(SA::fragment(sa, ra[i], kk));
-          }
-        }
-      }
-    }
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma<TYPE>(fb[set][j], fa[set][i], acc[i][j]);
   };
 
   // Slice s is there once this wave has only the loads of later slices
-  // outstanding and every wave has passed the barrier; the buffer that is filled next
-  // was last read in step s - 1, which every wave had finished (its LDS reads
-  // included) before the barrier.
-#pragma unroll
-  for (int s = 0; s < NSTAGE - 1; ++s)
-    if (s < slices) issue(s);
-  for (int s = 0; s < slices; ++s) {
-    wait_slices<PER, NSTAGE>(min(NSTAGE - 2, slices - 1 - s));
+  // outstanding and every wave has passed a barrier.
+  auto reduce = [&](auto works) {
+    constexpr bool WORKS = decltype(works)::value;
+    if (slices == 0) return;
+    wait_slices<PER, NSTAGE + 1>(min(NSTAGE - 1, slices - 1));
     block_barrier();
-    if (s + NSTAGE - 1 < slices) issue(s + NSTAGE - 1);
-    compute(s);
-  }
+    if constexpr (WORKS) read(0, 0, 0);
+#pragma unroll 1
+    for (int s = 0; s < slices; ++s) {
+      if constexpr (GRAD && WORKS) {
+        if (summing && (sharers == 1 || (s0 + s) % sharers == across)) {
+          const LIN_LDS char* sa = stage_of(s);
+#pragma unroll
+          for (int t = 0; t < STEPS; ++t) {
+            const int kk = WK == 1 ? t : t * WK + wk;
+            if (a.sum_side == 1) {
+#pragma unroll
+              for (int j = 0; j < TN; ++j) sum[j] += fragment_sum<TYPE>(SB::fragment(sa + SA::BYTES, rb[j], kk));
+            } else {
+#pragma unroll
+              for (int i = 0; i < TM; ++i) sum[i] += fragment_sum<TYPE>(SA::fragment(sa, ra[i], kk));
+            }
+          }
+        }
+      }
+      if constexpr (WORKS) {
+#pragma unroll
+        for (int t = 0; t < STEPS - 1; ++t) {
+          read(s, t + 1, (t + 1) & 1);
+          multiply(t & 1);
+        }
+      }
+      if (s + 1 < slices) {
+        // every wave has read all of slice s once it is here: its buffer is filled anew
+        wait_slices<PER, NSTAGE>(min(NSTAGE - 2, slices - 2 - s));
+        block_barrier();
+        if (s + NSTAGE < slices) issue(s + NSTAGE);
+        if constexpr (WORKS && STEPS > 1) read(s + 1, 0, 0);
+      }
+      if constexpr (WORKS) {
+        multiply((STEPS - 1) & 1);
+        if (STEPS == 1 && s + 1 < slices) read(s + 1, 0, 0);
+      }
+    }
+  };
+  // A wave whose part of the tile lies outside the output only helps to load.
+  if (row0 + wi * WTM >= a.m || col0 + wj * WTN >= a.n) reduce(std::false_type{});
+  else reduce(std::true_type{});
   wait_loads<0>();
   block_barrier();
 
   // The sums go through LDS, 32 rows of each wave at a time, and are stored in
-  // eights of consecutive columns, whole lines of the output.
-  LIN_LDS char* staged = (LIN_LDS char*)lds + wave * (32 * PITCH);
-  LIN_LDS char* first = (LIN_LDS char*)lds + (wave % (WM * WN)) * (32 * PITCH);  // of the wave tile's group wk = 0
+  // eights of consecutive columns, whole lines of the output: stored from
+  // registers, 32 bytes to a row, a 16-bit output cost up to 1.4 times as much in all.
+  constexpr int PART = 32 * PITCH, WAVE = AHEAD * PART, GROUP = WM * WN * WAVE;
+  LIN_LDS char* staged = (LIN_LDS char*)lds + wave * WAVE;
+  LIN_LDS char* first = (LIN_LDS char*)lds + (wave % (WM * WN)) * WAVE;  // of the wave tile's group wk = 0
   constexpr int EIGHTS = WTN / 8;
+  constexpr int MINE = 32 * EIGHTS / (64 * WK);  // eights of a lane in a part
+  static_assert(MINE * 64 * WK == 32 * EIGHTS, "each group of waves stores a share of the sums");
+  static_assert(PARTS % AHEAD == 0, "parts");
+  constexpr bool ONE_COL = (64 * WK) % EIGHTS == 0;  // a lane's eights lie in the same columns
   const bool to_part = GRAD && a.splits > 1;
   const int rows = to_part ? a.tiles_m * BM : a.m, cols = to_part ? a.tiles_n * BN : a.n;
+  const bool whole = row0 + BM <= rows && col0 + BN <= cols;
   auto stored = [&](auto&& store) {
+    typedef typename std::remove_reference<decltype(store)>::type Store;
+    auto place = [&](int t, int* r, int* c) {
+      const int q = (t * WK + wk) * 64 + lane;
+      *r = q / EIGHTS;
+      *c = q % EIGHTS;
+    };
+    f32x8 bias = 0.0f;
+    if constexpr (ONE_COL) {
+      const int col = col0 + wj * WTN + lane % EIGHTS * 8;
+      if (whole || col + 8 <= cols) bias = store.bias(col);
+    }
+    typename Store::Fetched got[MINE];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int t = 0; t < MINE; ++t) {
+        int r, c;
+        place(t, &r, &c);
+        const int row = row0 + wi * WTM + i * 32 + r, col = col0 + wj * WTN + c * 8;
+        if (whole || (row < rows && col + 8 <= cols)) got[t] = store.fetch(row, col);
+      }
+    };
+    fetch(0);
 #pragma unroll 1
-    for (int i = 0; i < TM; ++i) {
-      f32x16 v[TN];
-#pragma unroll
-      for (int q = 0; q < TM; ++q)
-        if (q == i) {
-#pragma unroll
-          for (int j = 0; j < TN; ++j) v[j] = acc[q][j];
+    for (int i = 0; i < PARTS; ++i) {
+      if (AHEAD == 1 || i % AHEAD == 0) {
+        if (WK > 1 && i > 0) {  // the parts before have been read
+          wait_loads<63>();
+          block_barrier();
         }
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+        for (int p = 0; p < AHEAD; ++p)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *(LIN_LDS f32x4*)(staged + (lane & 31) * PITCH + (j * 32 + 8 * e + 4 * (lane >> 5)) * 4) =
-              f32x4{v[j][4 * e], v[j][4 * e + 1], v[j][4 * e + 2], v[j][4 * e + 3]};
-      wait_loads<63>();  // LDS only
-      if (WK > 1) block_barrier(); else asm volatile("" ::: "memory");
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < 32 * EIGHTS / (64 * WK); ++t) {
-        const int q = (t * WK + wk) * 64 + lane, r = q / EIGHTS, c = q % EIGHTS;
-        const LIN_LDS char* at = first + r * PITCH + c * 32;
+            for (int j = 0; j < TN; ++j) {
+              f32x4 v;  // chosen as values: an array in registers takes no index
+#pragma unroll
+              for (int q = p; q < PARTS; q += AHEAD)
+                if (q == i + p) v = acc[2 * q + h][j];
+              *(LIN_LDS f32x4*)(staged + p * PART + (16 * h + (lane & 15)) * PITCH + (j * 16 + 4 * (lane >> 4)) * 4) = v;
+            }
+        if (WK > 1) {
+          wait_loads<63>();
+          block_barrier();
+        }
+      }
+      const LIN_LDS char* part = first + i % AHEAD * PART;
+#pragma unroll
+      for (int t = 0; t < MINE; ++t) {
+        int r, c;
+        place(t, &r, &c);
+        const LIN_LDS char* at = part + r * PITCH + c * 32;
         const int row = row0 + wi * WTM + i * 32 + r, col = col0 + wj * WTN + c * 8;
-        if (row >= rows) continue;
-        if (col + 8 <= cols) {
+        if (whole || (row < rows && col + 8 <= cols)) {
           f32x8 x = 0.0f;
 #pragma unroll
           for (int w = 0; w < WK; ++w) {
-            const LIN_LDS char* p = at + w * (WM * WN * 32 * PITCH);
-            const f32x4 lo = *(const LIN_LDS f32x4*)p, hi = *(const LIN_LDS f32x4*)(p + 16);
+            const LIN_LDS f32x4* p = (const LIN_LDS f32x4*)(at + w * GROUP);
+            const f32x4 lo = p[0], hi = p[1];
             const f32x8 y = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             x = w == 0 ? y : x + y;
           }
-          store(row, col, x);
-        } else {  // the last columns, one by one
-#pragma unroll 1
-          for (int k = 0; col + k < cols; ++k) {
-            float x = *(const LIN_LDS float*)(at + 4 * k);
+          store(row, col, x, ONE_COL ? bias : store.bias(col), got[t]);
+        }
+      }
+      if (!whole && cols % 8 != 0) {  // the last columns, one by one
+        const int c = (cols - col0 - wj * WTN) / 8;  // the eight that they are in
+        const int left = cols - (col0 + wj * WTN + c * 8);
+        if (c >= 0 && c < EIGHTS && left > 0) {
+          for (int q = wk * 64 + lane; q < 32 * left; q += 64 * WK) {
+            const int r = q / left, k = q - r * left, row = row0 + wi * WTM + i * 32 + r;
+            if (row >= rows) continue;
+            const LIN_LDS char* at = part + r * PITCH + c * 32 + k * 4;
+            float x = *(const LIN_LDS float*)at;
 #pragma unroll
-            for (int w = 1; w < WK; ++w) x += *(const LIN_LDS float*)(at + 4 * k + w * (WM * WN * 32 * PITCH));
-            store.one(row, col + k, x);
+            for (int w = 1; w < WK; ++w) x += *(const LIN_LDS float*)(at + w * GROUP);
+            store.one(row, col0 + wj * WTN + c * 8 + k, x);
           }
         }
       }
-      wait_loads<63>();
-      if (WK > 1) block_barrier(); else asm volatile("" ::: "memory");
+      if (i + 1 < PARTS) fetch(i + 1);
     }
   };
   if constexpr (!GRAD) {
-    stored(LayerStore<TYPE>(a));
+    const DropKey key(a.e);
+    if (a.e.backward) {
+      switch (a.e.act) {
+        case LIN_ACT_NONE: stored(LayerStore<TYPE, LIN_ACT_NONE, true>(a.e, key)); break;
+        case LIN_ACT_GELU: stored(LayerStore<TYPE, LIN_ACT_GELU, true>(a.e, key)); break;
+        case LIN_ACT_RELU: stored(LayerStore<TYPE, LIN_ACT_RELU, true>(a.e, key)); break;
+        default: stored(LayerStore<TYPE, LIN_ACT_RELU2, true>(a.e, key));
+      }
+    } else {
+      switch (a.e.act) {
+        case LIN_ACT_NONE: stored(LayerStore<TYPE, LIN_ACT_NONE, false>(a.e, key)); break;
+        case LIN_ACT_GELU: stored(LayerStore<TYPE, LIN_ACT_GELU, false>(a.e, key)); break;
+        case LIN_ACT_RELU: stored(LayerStore<TYPE, LIN_ACT_RELU, false>(a.e, key)); break;
+        default: stored(LayerStore<TYPE, LIN_ACT_RELU2, false>(a.e, key));
+      }
+    }
   } else {
     if (to_part) {
       const int64_t ld = (int64_t)a.tiles_n * BN;
@@ -405,15 +517,17 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void linear_gemm_kernel(const Li
       stored(GradStore{a.c, a.ldc, a.add != 0});
     }
     if (a.sum_side != 0) {
-      const int edge = a.sum_side == 1 ? BN : BM, wt = a.sum_side == 1 ? WTN : WTM, frags = wt / 32;
+      const int edge = a.sum_side == 1 ? BN : BM, wt = a.sum_side == 1 ? WTN : WTM, frags = wt / 16;
       LIN_LDS float* red = (LIN_LDS float*)lds;  // WK x edge
+      wait_loads<63>();
       block_barrier();
       if (summing) {
 #pragma unroll
         for (int f = 0; f < TS; ++f) {
           if (f >= frags) break;
-          const float v = sum[f] + __shfl_xor(sum[f], 32);
-          if (lane < 32) red[wk * edge + (a.sum_side == 1 ? wj : wi) * wt + f * 32 + lane] = v;
+          float v = sum[f] + __shfl_xor(sum[f], 32);
+          v += __shfl_xor(v, 16);
+          if (lane < 16) red[wk * edge + (a.sum_side == 1 ? wj : wi) * wt + f * 16 + lane] = v;
         }
       }
       wait_loads<63>();

@@ -118,29 +118,60 @@ LinOperand operand_of(const Matrix& m, int type, LinPlan* plan, void* workspace)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tiles, slices and splits of a product.
+// Microseconds of a round of tiles over the 256 compute units, as measured (bf16, one MI355X):
+// with `slices` K slices of 64, a start and an end and so much for each slice;
+// one tile to a unit, or the two that small tiles leave room for.  Over 12 slices a
+// round of 256 x 256 tiles takes 26.6, of 128 x 128 13.2 and 19, of 64 x 64 7.7 and
+// 10.6, of 32 x 64 6.8 and 8.2; over 48 77, 35 and 49, 20.7 and 30, 17.3 and 20.
+struct TileCost {
+  double one, one_slice, two, two_slice;  // two = 0: no second tile fits
+};
+constexpr TileCost kTileCost[LIN_TILES] = {{9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.4, 0.36, 4.0, 0.55}, {3.3, 0.29, 3.8, 0.36}};
+
+double tiles_us(int tile, int64_t tiles, int64_t slices) {
+  const TileCost& c = kTileCost[tile];
+  const double one = c.one + c.one_slice * (double)slices, two = c.two + c.two_slice * (double)slices;
+  if (c.two == 0) return (double)((tiles + 255) / 256) * one;
+  const int64_t rest = tiles % 512;
+  return (double)(tiles / 512) * two + (rest > 256 ? two : rest > 0 ? one : 0);
+}
+
+// A split leaves its sums in memory and a last pass adds them up: 3 us for the
+// launch, and the sums written and read at 5 TB/s.
+double splits_us(int64_t m, int64_t n, int64_t splits) { return splits == 1 ? 0 : 3.0 + (double)(m * n * splits) * 8 / 5e6; }
+
+// Tiles, slices and splits of a product: what the measured times make the
+// fastest.  Examples (us, chosen and next): 16384 x 3072 over 768 82 in 256 x 256
+// tiles, 90 in 128 x 128; 8192 x 2304 over 768 43 in 128 x 128, 55 in 256 x 256;
+// 512 x 768 over 3072 18.6 in 32 x 64, 20.7 in 64 x 64, 35 in 128 x 128.
 int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
   LinGemmArgs& g = p->gemm;
-  p->tile = LIN_TILE_128;
-  const LinTileSize t = kLinTile[p->tile];
   g.m = (int32_t)m;
   g.n = (int32_t)n;
   g.k = (int32_t)k;
   g.slices = ceil_div(k, LIN_BK);
-  const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn;
-  int splits = 1;
-  if (grad) {
-    // a split leaves its sums in memory and a last pass reads them: only as
-    // many as fill the compute units, of at least 8 slices each
-    const int64_t fill = 256 / (tm * tn);
-    splits = (int)std::max<int64_t>(1, std::min<int64_t>(fill, g.slices / 8));
+  double best = 0;
+  for (int tile = 0; tile < LIN_TILES; ++tile) {
+    if (grad && tile == LIN_TILE_32) continue;  // few rows of a weight are no case worth a kernel
+    const LinTileSize t = kLinTile[tile];
+    const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn, tiles = tm * tn;
+    for (int fill = 0; fill <= (grad ? 2 : 0); ++fill) {  // no splits, or as many as make one or two rounds
+      const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, g.slices / 4);
+      if (fill > 0 && want < 2) continue;
+      const int per = g.slices ? ceil_div(g.slices, want) : 0, splits = g.slices ? ceil_div(g.slices, per) : 1;
+      const double us = tiles_us(tile, tiles * splits, per) + splits_us(m, n, splits);
+      if (best != 0 && us >= best) continue;
+      best = us;
+      p->tile = tile;
+      g.per_split = per;
+      g.splits = splits;
+      g.tiles_m = (int32_t)std::min<int64_t>(tm, INT32_MAX);
+      g.tiles_n = (int32_t)tn;
+    }
   }
-  g.per_split = g.slices ? ceil_div(g.slices, splits) : 0;
-  g.splits = g.slices ? ceil_div(g.slices, g.per_split) : 1;
   // a grid holds fewer than 2^32 threads
-  if (tm * tn * g.splits >= (1 << 22)) return fail(MUON_EINVAL, "a product of %lld x %lld is too large", (long long)m, (long long)n);
-  g.tiles_m = (int32_t)tm;
-  g.tiles_n = (int32_t)tn;
+  if ((int64_t)g.tiles_m * g.tiles_n * g.splits >= ((int64_t)1 << 32) / kLinTile[p->tile].threads)
+    return fail(MUON_EINVAL, "a product of %lld x %lld is too large", (long long)m, (long long)n);
   return MUON_OK;
 }
 
@@ -214,6 +245,10 @@ int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool size
   e.act = l->act;
   e.backward = backward;
   fill_dropout(&e, l->dropout, l->seed, l->step, l->site, l->rng);
+  // What does not stay in the memory-side cache (256 MiB) until it is read goes
+  // past the caches: 32768 x 6400 y and z over 1600 712 us so and 755 us through
+  // them; 16384 x 3072 over 768, which does stay, 105 and 102.
+  e.stream = l->m * out * ((l->y_type == MUON_FP32 ? 4 : 2) + (l->preact && !backward ? 2 : 0)) > ((int64_t)256 << 20);
   return MUON_OK;
 }
 

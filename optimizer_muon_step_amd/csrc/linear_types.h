@@ -35,6 +35,7 @@ struct LinEpilogue {
   int32_t bias_type, y_type;
   int32_t act;
   int32_t backward;
+  int32_t stream;  // what is written goes past the caches
 };
 
 // An operand as the products read it: 16-bit elements, 16-byte aligned, rows of
@@ -107,11 +108,11 @@ struct LinFinishArgs {
 constexpr int FINISH_THREADS = 256;
 
 // Output tiles of the product kernels (see kernels_linear.hip and linear_host.cpp).
-enum LinTile { LIN_TILE_128 = 0, LIN_TILES };
+enum LinTile { LIN_TILE_256 = 0, LIN_TILE_128, LIN_TILE_64, LIN_TILE_32, LIN_TILES };
 struct LinTileSize {
-  int bm, bn;
+  int bm, bn, threads;
 };
-constexpr LinTileSize kLinTile[LIN_TILES] = {{128, 128}};
+constexpr LinTileSize kLinTile[LIN_TILES] = {{256, 256, 512}, {128, 128, 256}, {64, 64, 512}, {32, 64, 256}};
 
 // Dropout by itself.
 struct DropArgs {

@@ -75,6 +75,29 @@ def test_linear_shapes(shape, order, kind):
     check_linear(mu, x, w, kind, out="fp32", bias=b, act="gelu", keep=True, what="gelu")
 
 
+LARGE = [(4097, 72, 2311), (4160, 136, 2304), (1500, 72, 1304), (2000, 200, 1100), (3000, 72, 264)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("order", ["rows", "columns"])
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_large_tiles(shape, order, kind):
+    """Shapes that take the large tiles, with ragged ends, in all three products."""
+    import optimizer_muon_step_amd as mu
+    m, k, n = shape
+    rng = np.random.default_rng(m + n)
+    say(f"[large tiles] {shape} {order} {kind}")
+    x, w = make(rng, (m, k), kind), make(rng, (k, n), kind, 0.1, order=order)
+    res = make(rng, (m, n), kind)
+    check_linear(mu, x, w, kind, bias=make(rng, (1, n), "fp32")[0], act="gelu", drop=(0.1, 5, 6, 7), residual=res, keep=True)
+    check_linear(mu, x, w, kind, out="fp32", act="relu2")
+    # the same sizes with the roles of k and m in their places for the backward products
+    dz, wt = make(rng, (m, k), kind, 0.1), make(rng, (n, k), kind, 0.1, order=order)
+    check_dx(mu, dz, wt, kind, act="gelu", preact=make(rng, (m, n), kind), residual=res)
+    x, dz = make(rng, (k, m), kind), make(rng, (k, n), kind, 0.1)
+    check_dw(mu, x, dz, make(rng, (m, n), "fp32", order=order), kind, bias=True, add=True)
+
+
 @pytest.mark.parametrize("act", [None, "gelu", "relu", "relu2"])
 @pytest.mark.parametrize("parts", ["", "bias", "residual", "drop", "bias residual drop keep"])
 @pytest.mark.parametrize("out", ["same", "fp32"])
@@ -185,7 +208,7 @@ def check_dw(mu, x, dz, dw, kind, bias=False, add=False, what="dw"):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("order", ["rows", "columns"])
-@pytest.mark.parametrize("shape", SHAPES + [(4100, 72, 200), (9000, 264, 136), (20000, 8, 8), (3001, 131, 300)], ids=str)
+@pytest.mark.parametrize("shape", SHAPES + [(4100, 72, 200), (9000, 264, 136), (20000, 8, 8), (3001, 131, 300), (30000, 520, 264), (8200, 1040, 520)], ids=str)
 def test_dw_shapes(shape, order, kind):
     """The last ones are long enough for the reduction to be split."""
     import optimizer_muon_step_amd as mu
