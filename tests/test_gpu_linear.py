@@ -362,3 +362,61 @@ def test_versions_and_results():
     assert dw._version > before[0] and db._version > before[1]
     assert mu.muon_linear(x, w, residual=torch.ones(4, 16, device="cuda")).dtype == torch.float32
     assert z._version == before[2]
+
+
+def test_refusals_on_the_gpu():
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    half = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    x, w, y = half(4, 8), half(8, 16), half(4, 16)
+    f32 = torch.zeros
+    for match, call in [
+            ("x: float32, expected bfloat16 or float16", lambda: mu.muon_linear(x.float(), w)),
+            ("w: float16", lambda: mu.muon_linear(x, w.half())),
+            ("last dimension of 8, w is 16 x 8", lambda: mu.muon_linear(x, w.T)),
+            ("expected a matrix", lambda: mu.muon_linear(x, w[0])),
+            ("adjacent elements along one", lambda: mu.muon_linear(x, half(16, 32)[::2, ::2])),
+            ("adjacent elements along the last", lambda: mu.muon_linear(half(4, 16)[:, ::2], w)),
+            ("evenly spaced", lambda: mu.muon_linear(half(4, 6, 16)[:, :3, :8], w)),
+            ("bias", lambda: mu.muon_linear(x, w, bias=half(8))),
+            ("bias", lambda: mu.muon_linear(x, w, bias=half(32)[::2])),
+            ("bias: float16", lambda: mu.muon_linear(x, w, bias=half(16).half())),
+            ("residual: shape", lambda: mu.muon_linear(x, w, residual=half(4, 8))),
+            ("residual: bfloat16, expected float32", lambda: mu.muon_linear(x, w, residual=y, out_dtype=torch.float32)),
+            ("out: shape", lambda: mu.muon_linear(x, w, out=half(16, 4))),
+            ("out: float16", lambda: mu.muon_linear(x, w, out=y.half())),
+            ("out: its type", lambda: mu.muon_linear(x, w, out=y, out_dtype=torch.float32)),
+            ("preact: float32", lambda: mu.muon_linear(x, w, preact=y.float())),
+            ("on the GPU", lambda: mu.muon_linear(x, w.cpu())),
+            ("rng: dropout needs", lambda: mu.muon_linear(x, w, dropout=0.5)),
+            ("rng: expected", lambda: mu.muon_linear(x, w, dropout=0.5, rng=5)),
+            ("rng: expected", lambda: mu.muon_linear(x, w, dropout=0.5, rng=(1, 2, 3))),
+            ("rng: expected", lambda: mu.muon_linear(x, w, dropout=0.5, rng=torch.zeros(2, dtype=torch.int64))),
+            ("rng: expected", lambda: mu.muon_linear(x, w, dropout=0.5, rng=f32(2, device="cuda"))),
+            ("rng: seed", lambda: mu.muon_linear(x, w, dropout=0.5, rng=(-1, 0))),
+            ("rng: seed", lambda: mu.muon_linear(x, w, dropout=0.5, rng=(1.5, 0))),
+            ("rng: step", lambda: mu.muon_linear(x, w, dropout=0.5, rng=(1, 2 ** 32))),
+            ("site", lambda: mu.muon_linear(x, w, dropout=0.5, rng=(1, 2), site=-1)),
+            ("dz: last dimension", lambda: mu.muon_linear_dx(x, w)),
+            ("dw: expected 8 x 16", lambda: mu.muon_linear_dw(x, y, f32(16, 8, device="cuda"))),
+            ("dw: bfloat16", lambda: mu.muon_linear_dw(x, y, w)),
+            ("dz: float16", lambda: mu.muon_linear_dw(x, y.half(), w.float())),
+            ("dimensions before the last", lambda: mu.muon_linear_dw(x, half(5, 16), w.float())),
+            ("dbias", lambda: mu.muon_linear_dw(x, y, w.float(), dbias=f32(8, device="cuda"))),
+            ("preact: shape", lambda: mu.muon_dropout(x, 0.5, (1, 2), act="relu", preact=y)),
+            ("preact: bfloat16", lambda: mu.muon_dropout(x.float(), 0.5, (1, 2), act="relu", preact=x)),
+            ("rng: dropout needs", lambda: mu.muon_dropout(x, 0.5, None)),
+            ("hipStreamPerThread", lambda: mu.muon_linear(x, w, stream=2))]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    for match, call in [
+            ("overlap", lambda: mu.muon_linear(x, half(8, 8), out=x)),
+            ("overlap", lambda: mu.muon_linear(x, w, out=half(1, 16).expand(4, 16))),
+            ("dropout = 1", lambda: mu.muon_linear(x, w, dropout=1.0, rng=(1, 2))),
+            ("dropout = nan", lambda: mu.muon_dropout(x, float("nan"), (1, 2))),
+            ("come together", lambda: mu.muon_linear_dx(y, w, act="gelu")),
+            ("come together", lambda: mu.muon_dropout(x, 0.5, (1, 2), preact=x)),
+            ("overlaps", lambda: mu.muon_linear(x, w, out=y, preact=y))]:
+        with pytest.raises(mu.MuonError, match=match):
+            call()
+    torch.cuda.synchronize()
