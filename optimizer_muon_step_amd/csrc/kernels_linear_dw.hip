@@ -41,11 +41,20 @@ __global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const Lin
   const int64_t row = i / eights;
   if (row >= a.m) return;
   const int col = (int)(i - row * eights) * 8, have = min(8, a.n - col);
-  f32x8 v = load8<GRAD_FP32>(a.part, row * a.part_ld + col);  // its rows are padded to whole tiles
-  for (int s = 1; s < a.splits; ++s) v += load8<GRAD_FP32>(a.part + s * a.part_stride, row * a.part_ld + col);
-  const GradStore store = {a.c, a.ldc, a.add != 0};
+  const float* at = a.part + row * a.part_ld + col;  // its rows are padded to whole tiles
+  f32x8 v = load8<GRAD_FP32>(at, 0);
+  for (int s = 1; s < a.splits; s += 4) {  // four loads at a time
+    f32x8 more[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s + k < a.splits) more[k] = load8<GRAD_FP32>(at, (s + k) * a.part_stride);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s + k < a.splits) v += more[k];
+  }
+  const GradEdge store = {a.c, a.ldc, a.add != 0};
   if (have == 8) {
-    store(row, col, v, 0.0f, store.fetch(row, col));
+    store.eight(row, col, v);
   } else {
 #pragma unroll
     for (int k = 0; k < 7; ++k)

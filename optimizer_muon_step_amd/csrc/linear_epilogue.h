@@ -149,6 +149,18 @@ __device__ __forceinline__ f32x8 slope8(f32x8 z) {
   return z;
 }
 
+// By an activation known at run time.
+__device__ __forceinline__ f32x8 act8(f32x8 v, int act) {
+  if (act == LIN_ACT_GELU) return act8<LIN_ACT_GELU>(v);
+  if (act == LIN_ACT_RELU) return act8<LIN_ACT_RELU>(v);
+  return act == LIN_ACT_RELU2 ? act8<LIN_ACT_RELU2>(v) : v;
+}
+__device__ __forceinline__ f32x8 slope8(f32x8 z, int act) {
+  if (act == LIN_ACT_GELU) return slope8<LIN_ACT_GELU>(z);
+  if (act == LIN_ACT_RELU) return slope8<LIN_ACT_RELU>(z);
+  return slope8<LIN_ACT_RELU2>(z);
+}
+
 // ---- the mask ----
 // 128 bits of the counter (group, row, site, step) under the key.
 __device__ __forceinline__ u32x4 philox(uint32_t group, uint32_t row, uint32_t site, uint32_t step, uint32_t k0, uint32_t k1) {

@@ -176,79 +176,132 @@ __device__ __forceinline__ float fragment_sum(s16x8 f) {
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
-// What a tile's sums become: eight of them at (row, col ..), or one.  What an eight
-// needs from memory is fetched ahead of it.  ACT and BACKWARD are the launch's.
-template <int TYPE, int ACT, bool BACKWARD>
+// What a tile's sums become: eights of them at (row + d, col ..), from one place
+// of a lane on.  What an eight needs from memory is fetched ahead of it.  ACT and
+// BACKWARD are the launch's, RES whether it has a residual of y's 16-bit type (an
+// fp32 one is read where it is added, registers being short).
+template <int TYPE, int ACT, bool BACKWARD, bool RES>
 struct LayerStore {
+  static constexpr bool SLOPE = BACKWARD && ACT != LIN_ACT_NONE, FETCHES = SLOPE || RES;
   const LinEpilogue& e;
-  const DropKey key;
+  const DropKey& key;
   const bool wide;  // y and the residual are fp32
+  int64_t row, at_y, at_p, at_r;
+  int col;
+  f32x8 bias = 0.0f;
   struct Fetched {
-    u32x4 z, r;  // r: of a 16-bit residual; an fp32 one is read where it is added, registers being short
+    u32x4 z, r;
   };
-  __device__ __forceinline__ LayerStore(const LinEpilogue& e_, const DropKey& k) : e(e_), key(k), wide(e_.y_type == GRAD_FP32) {}
-
-  __device__ __forceinline__ Fetched fetch(int64_t row, int col) const {
+  __device__ __forceinline__ LayerStore(const LinEpilogue& e_, const DropKey& k, int row_, int col_)
+      : e(e_), key(k), wide(e_.y_type == GRAD_FP32), row(row_), col(col_) {
+    at_y = row * e.ldy + col;
+    at_p = row * e.ldp + col;
+    at_r = row * e.ldr + col;
+    if (!BACKWARD && e.bias) {
+      bias = e.bias_type == GRAD_FP32 ? load8<GRAD_FP32>(e.bias, col) : load8<TYPE>(e.bias, col);
+      asm volatile("" : "+v"(bias));  // waited for here, not after the stores of each part
+    }
+  }
+  __device__ __forceinline__ Fetched fetch(int d) const {
     Fetched f;
-    if constexpr (BACKWARD && ACT != LIN_ACT_NONE) f.z = load_raw<TYPE>(e.preact, row * e.ldp + col);
-    if (e.residual && !wide) f.r = load_raw<TYPE>(e.residual, row * e.ldr + col);
+    if constexpr (SLOPE) f.z = load_raw<TYPE>(e.preact, at_p + d * e.ldp);
+    if constexpr (RES) f.r = load_raw<TYPE>(e.residual, at_r + d * e.ldr);
     return f;
   }
-  // bias: of columns col .. col + 7, zeros where there is none
-  __device__ __forceinline__ f32x8 bias(int col) const {
-    if (BACKWARD || !e.bias) return 0.0f;
-    return e.bias_type == GRAD_FP32 ? load8<GRAD_FP32>(e.bias, col) : load8<TYPE>(e.bias, col);
+  // Until f is there.
+  __device__ __forceinline__ void wait(Fetched& f) const {
+    if constexpr (SLOPE) asm volatile("" : "+v"(f.z));
+    if constexpr (RES) asm volatile("" : "+v"(f.r));
   }
-  __device__ __forceinline__ void operator()(int64_t row, int col, f32x8 v, f32x8 bias, const Fetched& f) const {
+  __device__ __forceinline__ void put(int d, f32x8 v, const Fetched& f) const {
     if constexpr (!BACKWARD) {
       v += bias;
-      if (e.preact) store8<TYPE>(e.preact, row * e.ldp + col, v, e.stream);
+      if (e.preact) store8<TYPE>(e.preact, at_p + d * e.ldp, v, e.stream);
       v = act8<ACT>(v);
-    } else if constexpr (ACT != LIN_ACT_NONE) {
+    } else if constexpr (SLOPE) {
       v = slope8<ACT>(widen8<TYPE>(f.z)) * v;
     }
-    if (e.border != 0) v = drop8(e, key, row, col, v);
-    if (wide) {
-      if (e.residual) v = load8<GRAD_FP32>(e.residual, row * e.ldr + col) + v;
-      store8<GRAD_FP32>(e.y, row * e.ldy + col, v, e.stream);
+    if (e.border != 0) v = drop8(e, key, row + d, col, v);
+    if constexpr (RES) v = widen8<TYPE>(f.r) + v;
+    if (!RES && wide) {
+      if (e.residual) v = load8<GRAD_FP32>(e.residual, at_r + d * e.ldr) + v;
+      store8<GRAD_FP32>(e.y, at_y + d * e.ldy, v, e.stream);
     } else {
-      if (e.residual) v = widen8<TYPE>(f.r) + v;
-      store8<TYPE>(e.y, row * e.ldy + col, v, e.stream);
+      store8<TYPE>(e.y, at_y + d * e.ldy, v, e.stream);
+    }
+  }
+};
+
+// The same at the edges of the output: eights or single elements anywhere.
+template <int TYPE>
+struct LayerEdge {
+  const LinEpilogue& e;
+  const DropKey& key;
+  __device__ __forceinline__ void eight(int64_t row, int col, f32x8 v) const {
+    if (!e.backward) {
+      if (e.bias) v += e.bias_type == GRAD_FP32 ? load8<GRAD_FP32>(e.bias, col) : load8<TYPE>(e.bias, col);
+      if (e.preact) store8<TYPE>(e.preact, row * e.ldp + col, v);
+      v = act8(v, e.act);
+    } else if (e.act != LIN_ACT_NONE) {
+      v = slope8(load8<TYPE>(e.preact, row * e.ldp + col), e.act) * v;
+    }
+    if (e.border != 0) v = drop8(e, key, row, col, v);
+    if (e.y_type == GRAD_FP32) {
+      if (e.residual) v = load8<GRAD_FP32>(e.residual, row * e.ldr + col) + v;
+      store8<GRAD_FP32>(e.y, row * e.ldy + col, v);
+    } else {
+      if (e.residual) v = load8<TYPE>(e.residual, row * e.ldr + col) + v;
+      store8<TYPE>(e.y, row * e.ldy + col, v);
     }
   }
   static __device__ __forceinline__ float get1(int type, const void* p, int64_t i) {
     return type == GRAD_FP32 ? load1<GRAD_FP32>(p, i) : load1<TYPE>(p, i);
   }
   __device__ __forceinline__ void one(int64_t row, int col, float v) const {
-    if constexpr (!BACKWARD) {
+    if (!e.backward) {
       if (e.bias) v += get1(e.bias_type, e.bias, col);
       if (e.preact) store1<TYPE>(e.preact, row * e.ldp + col, v);
-      v = act_of<ACT>(v);
-    } else if constexpr (ACT != LIN_ACT_NONE) {
-      v *= act_slope<ACT>(load1<TYPE>(e.preact, row * e.ldp + col));
+      v = act_of(v, e.act);
+    } else if (e.act != LIN_ACT_NONE) {
+      v *= act_slope(load1<TYPE>(e.preact, row * e.ldp + col), e.act);
     }
     if (e.border != 0) v = drop1(e, key, row, col, v);
     if (e.residual) v = get1(e.y_type, e.residual, row * e.ldr + col) + v;
-    if (wide) store1<GRAD_FP32>(e.y, row * e.ldy + col, v);
+    if (e.y_type == GRAD_FP32) store1<GRAD_FP32>(e.y, row * e.ldy + col, v);
     else store1<TYPE>(e.y, row * e.ldy + col, v);
   }
 };
 
+template <bool ADD>
 struct GradStore {
+  static constexpr bool FETCHES = ADD;
   float* c;
-  int64_t ldc;
-  bool add;
+  int64_t ldc, at;
   struct Fetched {
     f32x8 c;
   };
-  __device__ __forceinline__ Fetched fetch(int64_t row, int col) const {
+  __device__ __forceinline__ GradStore(float* c_, int64_t ldc_, int row, int col) : c(c_), ldc(ldc_), at(row * ldc_ + col) {}
+  __device__ __forceinline__ Fetched fetch(int d) const {
     Fetched f;
-    if (add) f.c = load8<GRAD_FP32>(c, row * ldc + col);
+    if constexpr (ADD) f.c = load8<GRAD_FP32>(c, at + d * ldc);
     return f;
   }
-  __device__ __forceinline__ f32x8 bias(int) const { return 0.0f; }
-  __device__ __forceinline__ void operator()(int64_t row, int col, f32x8 v, f32x8, const Fetched& f) const {
-    store8<GRAD_FP32>(c, row * ldc + col, add ? f.c + v : v);
+  __device__ __forceinline__ void wait(Fetched& f) const {
+    if constexpr (ADD) asm volatile("" : "+v"(f.c));
+  }
+  __device__ __forceinline__ void put(int d, f32x8 v, const Fetched& f) const {
+    if constexpr (ADD) v = f.c + v;
+    store8<GRAD_FP32>(c, at + d * ldc, v);
+  }
+};
+
+struct GradEdge {
+  float* c;
+  int64_t ldc;
+  bool add;
+  __device__ __forceinline__ void eight(int64_t row, int col, f32x8 v) const {
+    if (add) v = load8<GRAD_FP32>(c, row * ldc + col) + v;
+    store8<GRAD_FP32>(c, row * ldc + col, v);
   }
   __device__ __forceinline__ void one(int64_t row, int col, float v) const {
     if (add) v = load1<GRAD_FP32>(c, row * ldc + col) + v;
@@ -273,7 +326,10 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
   constexpr int LDS = NSTAGE * STAGE > STAGED ? NSTAGE * STAGE : STAGED;
   static_assert(NSTAGE >= 2 && NSTAGE <= 8 && (NSTAGE - 1) * PER < 64 && LDS <= 160 * 1024, "ring");
   static_assert(STEPS >= 1 && STEPS * WK * 32 == BK && PARTS * 32 == WTM && TN * 16 == WTN, "wave tile");
-  static_assert(STEPS % 2 == 0 || STEPS == 1, "the two sets of fragments change places within a slice");
+  // Two sets of fragments, which change places within a slice, where registers
+  // allow; two k-major operands and the sums of one leave too few of them for 256 x 256.
+  constexpr bool READS_AHEAD = !(GRAD && TM * TN >= 32);
+  static_assert(STEPS % 2 == 0 || STEPS == 1, "see READS_AHEAD");
   __shared__ __attribute__((aligned(16))) char lds[LDS];
 
   const int lane = threadIdx.x & 63;
@@ -325,7 +381,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
   const int sharers = GRAD && a.splits > 1 ? (a.sum_side == 1 ? a.tiles_m : a.tiles_n) : 1;
   const bool summing = GRAD && ((a.sum_side == 1 && wi == 0) || (a.sum_side == 2 && wj == 0)) && (a.splits > 1 || across == 0);
 
-  s16x8 fa[2][TM], fb[2][TN];
+  s16x8 fa[READS_AHEAD ? 2 : 1][TM], fb[READS_AHEAD ? 2 : 1][TN];
   auto read = [&](int s, int step, int set) {
     const LIN_LDS char* sa = stage_of(s);
     const int kk = WK == 1 ? step : step * WK + wk;
@@ -349,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
     if (slices == 0) return;
     wait_slices<PER, NSTAGE + 1>(min(NSTAGE - 1, slices - 1));
     block_barrier();
-    if constexpr (WORKS) read(0, 0, 0);
+    if constexpr (WORKS && READS_AHEAD) read(0, 0, 0);
 #pragma unroll 1
     for (int s = 0; s < slices; ++s) {
       if constexpr (GRAD && WORKS) {
@@ -368,11 +424,17 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
           }
         }
       }
-      if constexpr (WORKS) {
+      if constexpr (WORKS && READS_AHEAD) {
 #pragma unroll
         for (int t = 0; t < STEPS - 1; ++t) {
           read(s, t + 1, (t + 1) & 1);
           multiply(t & 1);
+        }
+      } else if constexpr (WORKS) {
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+          read(s, t, 0);
+          if (t < STEPS - 1) multiply(0);
         }
       }
       if (s + 1 < slices) {
@@ -380,11 +442,11 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
         wait_slices<PER, NSTAGE>(min(NSTAGE - 2, slices - 2 - s));
         block_barrier();
         if (s + NSTAGE < slices) issue(s + NSTAGE);
-        if constexpr (WORKS && STEPS > 1) read(s + 1, 0, 0);
+        if constexpr (WORKS && READS_AHEAD && STEPS > 1) read(s + 1, 0, 0);
       }
       if constexpr (WORKS) {
-        multiply((STEPS - 1) & 1);
-        if (STEPS == 1 && s + 1 < slices) read(s + 1, 0, 0);
+        multiply(READS_AHEAD ? (STEPS - 1) & 1 : 0);
+        if (READS_AHEAD && STEPS == 1 && s + 1 < slices) read(s + 1, 0, 0);
       }
     }
   };
@@ -400,121 +462,130 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
   constexpr int PART = 32 * PITCH, WAVE = AHEAD * PART, GROUP = WM * WN * WAVE;
   LIN_LDS char* staged = (LIN_LDS char*)lds + wave * WAVE;
   LIN_LDS char* first = (LIN_LDS char*)lds + (wave % (WM * WN)) * WAVE;  // of the wave tile's group wk = 0
-  constexpr int EIGHTS = WTN / 8;
-  constexpr int MINE = 32 * EIGHTS / (64 * WK);  // eights of a lane in a part
-  static_assert(MINE * 64 * WK == 32 * EIGHTS, "each group of waves stores a share of the sums");
-  static_assert(PARTS % AHEAD == 0, "parts");
-  constexpr bool ONE_COL = (64 * WK) % EIGHTS == 0;  // a lane's eights lie in the same columns
-  const bool to_part = GRAD && a.splits > 1;
-  const int rows = to_part ? a.tiles_m * BM : a.m, cols = to_part ? a.tiles_n * BN : a.n;
-  const bool whole = row0 + BM <= rows && col0 + BN <= cols;
-  auto stored = [&](auto&& store) {
-    typedef typename std::remove_reference<decltype(store)>::type Store;
-    auto place = [&](int t, int* r, int* c) {
-      const int q = (t * WK + wk) * 64 + lane;
-      *r = q / EIGHTS;
-      *c = q % EIGHTS;
-    };
-    f32x8 bias = 0.0f;
-    if constexpr (ONE_COL) {
-      const int col = col0 + wj * WTN + lane % EIGHTS * 8;
-      if (whole || col + 8 <= cols) bias = store.bias(col);
-    }
-    typename Store::Fetched got[MINE];
-    auto fetch = [&](int i) {
+  constexpr int EIGHTS = WTN / 8, AT_ONCE = 64 / EIGHTS;  // eights of a row, rows of the wave's lanes
+  constexpr int MINE = 32 / (AT_ONCE * WK);               // eights of a lane in a part, AT_ONCE WK rows apart
+  static_assert(AT_ONCE * EIGHTS == 64 && MINE * AT_ONCE * WK == 32, "each group of waves stores a share of the sums");
+  static_assert((PARTS == AHEAD || PARTS == 2 * AHEAD) && (WK == 1 || PARTS == 1), "parts");
+  const int row1 = row0 + wi * WTM + wk * AT_ONCE + lane / EIGHTS, col1 = col0 + wj * WTN + lane % EIGHTS * 8;
+  const LIN_LDS char* mine = first + (wk * AT_ONCE + lane / EIGHTS) * PITCH + lane % EIGHTS * 32;
+  // Parts from p on to LDS (p is a constant wherever this is used: registers take no index).
+  auto stage = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < MINE; ++t) {
-        int r, c;
-        place(t, &r, &c);
-        const int row = row0 + wi * WTM + i * 32 + r, col = col0 + wj * WTN + c * 8;
-        if (whole || (row < rows && col + 8 <= cols)) got[t] = store.fetch(row, col);
-      }
-    };
-    fetch(0);
-#pragma unroll 1
-    for (int i = 0; i < PARTS; ++i) {
-      if (AHEAD == 1 || i % AHEAD == 0) {
-        if (WK > 1 && i > 0) {  // the parts before have been read
-          wait_loads<63>();
-          block_barrier();
-        }
+    for (int q = 0; q < AHEAD; ++q)
 #pragma unroll
-        for (int p = 0; p < AHEAD; ++p)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-              f32x4 v;  // chosen as values: an array in registers takes no index
-#pragma unroll
-              for (int q = p; q < PARTS; q += AHEAD)
-                if (q == i + p) v = acc[2 * q + h][j];
-              *(LIN_LDS f32x4*)(staged + p * PART + (16 * h + (lane & 15)) * PITCH + (j * 16 + 4 * (lane >> 4)) * 4) = v;
-            }
-        if (WK > 1) {
-          wait_loads<63>();
-          block_barrier();
-        }
-      }
-      const LIN_LDS char* part = first + i % AHEAD * PART;
-#pragma unroll
-      for (int t = 0; t < MINE; ++t) {
-        int r, c;
-        place(t, &r, &c);
-        const LIN_LDS char* at = part + r * PITCH + c * 32;
-        const int row = row0 + wi * WTM + i * 32 + r, col = col0 + wj * WTN + c * 8;
-        if (whole || (row < rows && col + 8 <= cols)) {
-          f32x8 x = 0.0f;
-#pragma unroll
-          for (int w = 0; w < WK; ++w) {
-            const LIN_LDS f32x4* p = (const LIN_LDS f32x4*)(at + w * GROUP);
-            const f32x4 lo = p[0], hi = p[1];
-            const f32x8 y = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            x = w == 0 ? y : x + y;
-          }
-          store(row, col, x, ONE_COL ? bias : store.bias(col), got[t]);
-        }
-      }
-      if (!whole && cols % 8 != 0) {  // the last columns, one by one
-        const int c = (cols - col0 - wj * WTN) / 8;  // the eight that they are in
-        const int left = cols - (col0 + wj * WTN + c * 8);
-        if (c >= 0 && c < EIGHTS && left > 0) {
-          for (int q = wk * 64 + lane; q < 32 * left; q += 64 * WK) {
-            const int r = q / left, k = q - r * left, row = row0 + wi * WTM + i * 32 + r;
-            if (row >= rows) continue;
-            const LIN_LDS char* at = part + r * PITCH + c * 32 + k * 4;
-            float x = *(const LIN_LDS float*)at;
-#pragma unroll
-            for (int w = 1; w < WK; ++w) x += *(const LIN_LDS float*)(at + w * GROUP);
-            store.one(row, col0 + wj * WTN + c * 8 + k, x);
-          }
-        }
-      }
-      if (i + 1 < PARTS) fetch(i + 1);
+        for (int j = 0; j < TN; ++j)
+          *(LIN_LDS f32x4*)(staged + q * PART + (16 * h + (lane & 15)) * PITCH + (j * 16 + 4 * (lane >> 4)) * 4) =
+              acc[2 * (p + q) + h][j];
+    if (WK > 1) {
+      wait_loads<63>();
+      block_barrier();
     }
   };
+  // An eight, `d` rows below this lane's first, of the parts that are staged.
+  auto staged_eight = [&](int d) __attribute__((always_inline)) {
+    f32x8 x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+      const LIN_LDS f32x4* p = (const LIN_LDS f32x4*)(mine + w * GROUP + d * PITCH);
+      const f32x4 lo = p[0], hi = p[1];
+      const f32x8 y = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      x = w == 0 ? y : x + y;
+    }
+    return x;
+  };
+  auto store_whole = [&](const auto& store) {
+    typedef typename std::remove_cv<typename std::remove_reference<decltype(store)>::type>::type Store;
+    typename Store::Fetched got[MINE], next[MINE];
+    if constexpr (Store::FETCHES) {
+#pragma unroll
+      for (int t = 0; t < MINE; ++t) got[t] = store.fetch(t * AT_ONCE * WK);
+    }
+#pragma unroll
+    for (int h = 0; h < PARTS; h += AHEAD) {
+      stage(h);
+#pragma clang loop unroll_count(GRAD ? AHEAD : 1)
+      for (int i = h; i < h + AHEAD; ++i) {
+        if constexpr (Store::FETCHES) {
+          // what the next part needs goes out before this part's stores: waiting for
+          // a load waits for all that went out before it
+#pragma unroll
+          for (int t = 0; t < MINE; ++t) {
+            store.wait(got[t]);
+            if (i + 1 < PARTS) next[t] = store.fetch(32 * (i + 1) + t * AT_ONCE * WK);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < MINE; ++t)
+          store.put(32 * i + t * AT_ONCE * WK, staged_eight(32 * (i - h) + t * AT_ONCE * WK), got[t]);
+        if constexpr (Store::FETCHES) {
+#pragma unroll
+          for (int t = 0; t < MINE; ++t) {
+            store.wait(next[t]);
+            got[t] = next[t];
+          }
+        }
+      }
+    }
+  };
+  auto store_edge = [&](const auto& edge) {
+#pragma unroll
+    for (int i = 0; i < PARTS; i += AHEAD) {
+      stage(i);
+#pragma unroll 1
+      for (int u = 0; u < AHEAD * MINE; ++u) {
+        const int d = u * AT_ONCE * WK, row = row1 + 32 * i + d;
+        if (row < a.m && col1 + 8 <= a.n) edge.eight(row, col1, staged_eight(d));
+      }
+      const int c = a.n / 8 * 8 - col0 - wj * WTN, left = a.n % 8;  // the last columns, one by one
+      if (left != 0 && c >= 0 && c < WTN) {
+        for (int q = wk * 64 + lane; q < AHEAD * 32 * left; q += 64 * WK) {
+          const int r = q / left, k = c + q - r * left, row = row0 + wi * WTM + 32 * i + r;
+          if (row >= a.m) continue;
+          const LIN_LDS char* at = first + r * PITCH + k * 4;
+          float x = *(const LIN_LDS float*)at;
+#pragma unroll
+          for (int w = 1; w < WK; ++w) x += *(const LIN_LDS float*)(at + w * GROUP);
+          edge.one(row, col0 + wj * WTN + k, x);
+        }
+      }
+    }
+  };
+  const bool whole = row0 + BM <= a.m && col0 + BN <= a.n;
   if constexpr (!GRAD) {
     const DropKey key(a.e);
-    if (a.e.backward) {
-      switch (a.e.act) {
-        case LIN_ACT_NONE: stored(LayerStore<TYPE, LIN_ACT_NONE, true>(a.e, key)); break;
-        case LIN_ACT_GELU: stored(LayerStore<TYPE, LIN_ACT_GELU, true>(a.e, key)); break;
-        case LIN_ACT_RELU: stored(LayerStore<TYPE, LIN_ACT_RELU, true>(a.e, key)); break;
-        default: stored(LayerStore<TYPE, LIN_ACT_RELU2, true>(a.e, key));
-      }
+    if (!whole) {
+      store_edge(LayerEdge<TYPE>{a.e, key});
     } else {
-      switch (a.e.act) {
-        case LIN_ACT_NONE: stored(LayerStore<TYPE, LIN_ACT_NONE, false>(a.e, key)); break;
-        case LIN_ACT_GELU: stored(LayerStore<TYPE, LIN_ACT_GELU, false>(a.e, key)); break;
-        case LIN_ACT_RELU: stored(LayerStore<TYPE, LIN_ACT_RELU, false>(a.e, key)); break;
-        default: stored(LayerStore<TYPE, LIN_ACT_RELU2, false>(a.e, key));
+      auto with_act = [&](auto backward, auto res) {
+        constexpr bool BWD = decltype(backward)::value, RES = decltype(res)::value;
+        switch (a.e.act) {
+          case LIN_ACT_NONE: store_whole(LayerStore<TYPE, LIN_ACT_NONE, BWD, RES>(a.e, key, row1, col1)); break;
+          case LIN_ACT_GELU: store_whole(LayerStore<TYPE, LIN_ACT_GELU, BWD, RES>(a.e, key, row1, col1)); break;
+          case LIN_ACT_RELU: store_whole(LayerStore<TYPE, LIN_ACT_RELU, BWD, RES>(a.e, key, row1, col1)); break;
+          default: store_whole(LayerStore<TYPE, LIN_ACT_RELU2, BWD, RES>(a.e, key, row1, col1));
+        }
+      };
+      const bool res = a.e.residual && a.e.y_type != GRAD_FP32;
+      if (a.e.backward) {
+        if (res) with_act(std::true_type{}, std::true_type{});
+        else with_act(std::true_type{}, std::false_type{});
+      } else {
+        if (res) with_act(std::false_type{}, std::true_type{});
+        else with_act(std::false_type{}, std::false_type{});
       }
     }
   } else {
-    if (to_part) {
+    const bool to_part = a.splits > 1;
+    if (to_part) {  // rows padded to whole tiles
       const int64_t ld = (int64_t)a.tiles_n * BN;
-      stored(GradStore{a.part + split * (ld * a.tiles_m * BM), ld, false});
+      store_whole(GradStore<false>(a.part + split * (ld * a.tiles_m * BM), ld, row1, col1));
+    } else if (whole) {
+      if (a.add) store_whole(GradStore<true>(a.c, a.ldc, row1, col1));
+      else store_whole(GradStore<false>(a.c, a.ldc, row1, col1));
     } else {
-      stored(GradStore{a.c, a.ldc, a.add != 0});
+      store_edge(GradEdge{a.c, a.ldc, a.add != 0});
     }
     if (a.sum_side != 0) {
       const int edge = a.sum_side == 1 ? BN : BM, wt = a.sum_side == 1 ? WTN : WTM, frags = wt / 16;
