@@ -14,8 +14,9 @@ static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
   switch (tile) {  // tile, K slice, waves along m, n and k, stages, blocks to a compute unit
     case LIN_TILE_256: linear_gemm_kernel<TYPE, false, BKM, false, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_128: linear_gemm_kernel<TYPE, false, BKM, false, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
-    case LIN_TILE_64: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 64, 2, 2, 2, 5, 2><<<grid, threads, 0, s>>>(a); break;
-    case LIN_TILE_32: linear_gemm_kernel<TYPE, false, BKM, false, 32, 64, 64, 1, 2, 2, 6, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_64: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 2, 2, 2, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_64_DEEP: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 1, 4, 4, 1><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_32: linear_gemm_kernel<TYPE, false, BKM, false, 32, 64, 128, 1, 1, 4, 3, 2><<<grid, threads, 0, s>>>(a); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -15,7 +15,7 @@ static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
   switch (tile) {  // as in kernels_linear.hip
     case LIN_TILE_256: linear_gemm_kernel<TYPE, true, true, true, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_128: linear_gemm_kernel<TYPE, true, true, true, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
-    case LIN_TILE_64: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 64, 2, 2, 2, 5, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_64: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 128, 2, 2, 2, 2, 2><<<grid, threads, 0, s>>>(a); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

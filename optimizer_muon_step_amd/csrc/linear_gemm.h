@@ -11,7 +11,7 @@
 //
 // Pipeline: WM x WN x WK waves over a BM x BN tile.  K advances in slices of
 // BK through a ring of NSTAGE LDS buffers that buffer loads fill directly (no
-// registers), every row segment a whole 128-byte line.  The fragments of a k-step
+// registers), every row segment whole 128-byte lines.  The fragments of a k-step
 // are read while the matrix cores work on the step before, across the slices'
 // borders too: the barrier that hands over the next slice stands before the last
 // k-step of the current one.  Buffer loads bound every access by the
@@ -94,16 +94,17 @@ struct Slice {
   static constexpr int PITCH = KMAJOR ? R * 2 : BK * 2;  // bytes of a row
   static constexpr int CHUNKS = PITCH / 16;  // 16-byte chunks of a row
   static_assert(R % 32 == 0 && LOADS >= 1 && LOADS * 1024 * NW == BYTES, "tile does not split into whole loads");
-  static_assert(BK == 64 || BK == 32, "k-contiguous rows of 128 or 64 bytes");
-  static_assert(!KMAJOR || R == 64 || R == 128 || R == 192 || R == 256, "k-major rows of 128, 256, 384 or 512 bytes");
+  static_assert(BK == 128 || BK == 64, "k-contiguous rows of 256 or 128 bytes");
+  static_assert(!KMAJOR || R == 64 || R == 128 || R == 256, "k-major rows of 128, 256 or 512 bytes");
 
-  // Chunk swizzle.  A k-contiguous fragment has 16 lanes on 16 rows at
-  // one chunk; two rows of 64 elements (four of 32) share a 256-byte line of the banks,
-  // so XOR by (row / 2) % 8 ((row / 4) % 4) puts the 16 reads on 16 chunks.  A transposing read has each 16 lanes on 4
-  // rows, 32 bytes each, and pairs of such groups 32 bytes apart; the XOR sends the
-  // 4 rows to different 64-byte groups of the banks.
+  // Chunk swizzle.  A k-contiguous fragment has 16 lanes on 16 rows at one
+  // chunk; a row of 128 elements fills a 256-byte line of the banks and two rows of
+  // 64 share one, so XOR by row % 16, or (row / 2) % 8, puts the 16 reads on 16
+  // chunks.  A transposing read has each 16 lanes on 4 rows, 32 bytes each, and the
+  // next 16 lanes 8 rows further on; the XOR sends the 4 rows to different 64-byte
+  // groups of the banks and the 8 rows to the other half of such a group.
   static __device__ __forceinline__ int swz(int row, int chunk) {
-    if (!KMAJOR) return BK == 64 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
+    if (!KMAJOR) return BK == 64 ? chunk ^ ((row >> 1) & 7) : chunk ^ (row & 15);
     return chunk ^ (PITCH % 256 != 0 ? 4 * ((row >> 1) & 1) : 4 * (row & 3)) ^ (2 * ((row >> 3) & 1));
   }
 

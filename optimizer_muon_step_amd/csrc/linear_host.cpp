@@ -119,18 +119,21 @@ LinOperand operand_of(const Matrix& m, int type, LinPlan* plan, void* workspace)
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Microseconds of a round of tiles over the 256 compute units, as measured (bf16, one MI355X):
-// with `slices` K slices of 64, a start and an end and so much for each slice;
-// one tile to a unit, or the two that small tiles leave room for.  Over 12 slices a
-// round of 256 x 256 tiles takes 26.6, of 128 x 128 13.2 and 19, of 64 x 64 7.7 and
-// 10.6, of 32 x 64 6.8 and 8.2; over 48 77, 35 and 49, 20.7 and 30, 17.3 and 20.
+// a start and an end and so much for each 64 of K; one tile to a unit, or the two
+// that small tiles leave room for.  Over a K of 768 a round of 256 x 256 tiles
+// takes 26.6, of 128 x 128 13.2 and 19, of 64 x 64 6.2 and 8.8, of 32 x 64 5.3 and
+// 6.9; over 3072 77, 35 and 49, 14 and 22, 12 and 16.  Two k-major operands (a weight
+// gradient's) take 1.17 of that a slice.
 struct TileCost {
   double one, one_slice, two, two_slice;  // two = 0: no second tile fits
 };
-constexpr TileCost kTileCost[LIN_TILES] = {{9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.4, 0.36, 4.0, 0.55}, {3.3, 0.29, 3.8, 0.36}};
+constexpr TileCost kTileCost[LIN_TILES] = {
+    {9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24}};
+constexpr double GRAD_SLICE = 1.17;
 
-double tiles_us(int tile, int64_t tiles, int64_t slices) {
+double tiles_us(int tile, int64_t tiles, double slices) {
   const TileCost& c = kTileCost[tile];
-  const double one = c.one + c.one_slice * (double)slices, two = c.two + c.two_slice * (double)slices;
+  const double one = c.one + c.one_slice * slices, two = c.two + c.two_slice * slices;
   if (c.two == 0) return (double)((tiles + 255) / 256) * one;
   const int64_t rest = tiles % 512;
   return (double)(tiles / 512) * two + (rest > 256 ? two : rest > 0 ? one : 0);
@@ -143,26 +146,32 @@ double splits_us(int64_t m, int64_t n, int64_t splits) { return splits == 1 ? 0 
 // Tiles, slices and splits of a product: what the measured times make the
 // fastest.  Examples (us, chosen and next): 16384 x 3072 over 768 82 in 256 x 256
 // tiles, 90 in 128 x 128; 8192 x 2304 over 768 43 in 128 x 128, 55 in 256 x 256;
-// 512 x 768 over 3072 18.6 in 32 x 64, 20.7 in 64 x 64, 35 in 128 x 128.
+// 1024 x 768 over 2304 11.4 in 64 x 64 with the deep ring, 12.6 with the other, 28
+// in 128 x 128; 512 x 768 over 3072 12.2 in 32 x 64, 13.4 in 64 x 64.
 int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
   LinGemmArgs& g = p->gemm;
   g.m = (int32_t)m;
   g.n = (int32_t)n;
   g.k = (int32_t)k;
-  g.slices = ceil_div(k, LIN_BK);
   double best = 0;
   for (int tile = 0; tile < LIN_TILES; ++tile) {
-    if (grad && tile == LIN_TILE_32) continue;  // few rows of a weight are no case worth a kernel
+    // few rows of a weight, or few weights over few rows, are no case worth a kernel
+    if (grad && (tile == LIN_TILE_32 || tile == LIN_TILE_64_DEEP)) continue;
+    // up to 32 rows it makes no more tiles, and each loads with fewer waves: one row of
+    // 2304 over 768 7.5 us, 5.5 in 64 x 64
+    if (tile == LIN_TILE_32 && m <= 32) continue;
     const LinTileSize t = kLinTile[tile];
     const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn, tiles = tm * tn;
+    const int slices = ceil_div(k, t.bk);
     for (int fill = 0; fill <= (grad ? 2 : 0); ++fill) {  // no splits, or as many as make one or two rounds
-      const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, g.slices / 4);
+      const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, slices * t.bk / 256);
       if (fill > 0 && want < 2) continue;
-      const int per = g.slices ? ceil_div(g.slices, want) : 0, splits = g.slices ? ceil_div(g.slices, per) : 1;
-      const double us = tiles_us(tile, tiles * splits, per) + splits_us(m, n, splits);
+      const int per = slices ? ceil_div(slices, want) : 0, splits = slices ? ceil_div(slices, per) : 1;
+      const double us = tiles_us(tile, tiles * splits, per * t.bk / 64.0 * (grad ? GRAD_SLICE : 1.0)) + splits_us(m, n, splits);
       if (best != 0 && us >= best) continue;
       best = us;
       p->tile = tile;
+      g.slices = slices;
       g.per_split = per;
       g.splits = splits;
       g.tiles_m = (int32_t)std::min<int64_t>(tm, INT32_MAX);

@@ -67,13 +67,12 @@ constexpr int64_t pack_blocks(const LinPack& p) {
 // LIN_GROUP tile rows, column by column within a group, and each XCD takes a run
 // of them: the 32 tiles that its compute units hold at a time then share 8
 // row panels and 4 column panels in its L2.
-constexpr int LIN_BK = 64;  // elements of a K slice
 constexpr int LIN_GROUP = 8;
 struct LinGemmArgs {
   LinOperand a, b;
   int32_t m, n, k;
   int32_t tiles_m, tiles_n;
-  int32_t slices;     // of K
+  int32_t slices;     // of K, of the tile's bk
   int32_t splits;     // of the slices; above 1 every split leaves its sums in part
   int32_t per_split;  // slices of a split
   LinEpilogue e;      // of the products of a layer
@@ -108,11 +107,13 @@ struct LinFinishArgs {
 constexpr int FINISH_THREADS = 256;
 
 // Output tiles of the product kernels (see kernels_linear.hip and linear_host.cpp).
-enum LinTile { LIN_TILE_256 = 0, LIN_TILE_128, LIN_TILE_64, LIN_TILE_32, LIN_TILES };
+// 64_DEEP has the ring of two compute units' share of 64.
+enum LinTile { LIN_TILE_256 = 0, LIN_TILE_128, LIN_TILE_64, LIN_TILE_64_DEEP, LIN_TILE_32, LIN_TILES };
 struct LinTileSize {
-  int bm, bn, threads;
+  int bm, bn, bk, threads;
 };
-constexpr LinTileSize kLinTile[LIN_TILES] = {{256, 256, 512}, {128, 128, 256}, {64, 64, 512}, {32, 64, 256}};
+constexpr LinTileSize kLinTile[LIN_TILES] = {
+    {256, 256, 64, 512}, {128, 128, 64, 256}, {64, 64, 128, 512}, {64, 64, 128, 512}, {32, 64, 128, 256}};
 
 // Dropout by itself.
 struct DropArgs {

@@ -63,7 +63,7 @@ static void check_gemm(const LinPlan& p, int64_t m, int64_t n, int64_t k) {
   CHECK(g.m == m && g.n == n && g.k == k);
   CHECK((int64_t)g.tiles_m * t.bm >= m && (int64_t)(g.tiles_m - 1) * t.bm < m);
   CHECK((int64_t)g.tiles_n * t.bn >= n && (int64_t)(g.tiles_n - 1) * t.bn < n);
-  CHECK((int64_t)g.slices * LIN_BK >= k && (int64_t)(g.slices - 1) * LIN_BK < k);
+  CHECK((int64_t)g.slices * t.bk >= k && (int64_t)(g.slices - 1) * t.bk < k);
   CHECK(g.splits >= 1 && (int64_t)g.splits * g.per_split >= g.slices && (g.splits - 1) * g.per_split < std::max(1, g.slices));
   for (const LinOperand* o : {&g.a, &g.b}) {
     if (k == 0) continue;
@@ -102,8 +102,10 @@ static void check_layers() {
   CHECK(tiles.size() == LIN_TILES);
   // the sizes by which the tests on the GPU mean to reach each tile
   LinPlan p;
-  CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_32);
-  CHECK(run(layer(300, 768, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_64);
+  CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_64_DEEP);
+  CHECK(run(layer(130, 200, 1000), false, &p) == MUON_OK && p.tile == LIN_TILE_32);
+  CHECK(run(layer(1500, 72, 1304), false, &p) == MUON_OK && p.tile == LIN_TILE_64);
+  CHECK(run(layer(1000, 2304, 760), false, &p) == MUON_OK && p.tile == LIN_TILE_64_DEEP);
   CHECK(run(layer(2000, 200, 1100), false, &p) == MUON_OK && p.tile == LIN_TILE_128);
   CHECK(run(layer(4097, 72, 2311), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
   CHECK(run(layer(4160, 136, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
@@ -293,7 +295,7 @@ static void check_grads() {
             }
           }
         }
-  CHECK(split && tiles.size() == 3 && !tiles.count(LIN_TILE_32));
+  CHECK(split && tiles.size() == 3 && !tiles.count(LIN_TILE_32) && !tiles.count(LIN_TILE_64_DEEP));
   LinPlan p;
   CHECK(run(grad(72, 4097, 2311), &p) == MUON_OK && p.tile == LIN_TILE_256);
   CHECK(run(grad(200, 2000, 1100), &p) == MUON_OK && p.tile == LIN_TILE_128);

@@ -75,7 +75,7 @@ def test_linear_shapes(shape, order, kind):
     check_linear(mu, x, w, kind, out="fp32", bias=b, act="gelu", keep=True, what="gelu")
 
 
-LARGE = [(4097, 72, 2311), (4160, 136, 2304), (1500, 72, 1304), (2000, 200, 1100), (3000, 72, 264)]
+LARGE = [(4097, 72, 2311), (4160, 136, 2304), (1500, 72, 1304), (2000, 200, 1100), (3000, 72, 264), (1000, 2304, 760)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
