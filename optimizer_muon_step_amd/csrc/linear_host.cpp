@@ -412,8 +412,8 @@ int plan_dropout(const muon_dropout_t* d, DropArgs* out, int64_t* blocks) {
   if ((rc = check_overlaps(all, may_be_y, n))) return rc;
   if (d->rng && d->dropout > 0.0f && overlap(all[0], Matrix{"rng", d->rng, 1, 4, 4, MUON_FP32, false}))
     return fail(MUON_EINVAL, "y overlaps rng");
-  const int64_t eights = d->m * ((d->n + 7) / 8), per_block = DROP_THREADS * DROP_CHUNKS;
-  *blocks = (eights + per_block - 1) / per_block;
+  const int64_t eights = d->m * ((d->n + 7) / 8);
+  *blocks = (eights + DROP_THREADS - 1) / DROP_THREADS;
   if (*blocks > MAX_LAUNCH_ITEMS) return fail(MUON_EINVAL, "%lld x %lld elements are too many", (long long)d->m, (long long)d->n);
   out->x = d->x;
   out->ldx = d->ldx;

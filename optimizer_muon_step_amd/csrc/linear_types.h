@@ -58,9 +58,9 @@ struct LinPackArgs {
   LinPack job[2];
   int32_t n;
 };
-constexpr int PACK_THREADS = 256, PACK_CHUNKS = 4;  // of 8 elements, per thread
+constexpr int PACK_THREADS = 256;  // 8 elements each
 constexpr int64_t pack_blocks(const LinPack& p) {
-  return (p.rows * ((p.cols + 7) / 8) + PACK_THREADS * PACK_CHUNKS - 1) / (PACK_THREADS * PACK_CHUNKS);
+  return (p.rows * ((p.cols + 7) / 8) + PACK_THREADS - 1) / PACK_THREADS;
 }
 
 // One product C = A B, m x n over k.  Output tiles are numbered in groups of
@@ -123,6 +123,6 @@ struct DropArgs {
   int32_t x_type;
   LinEpilogue e;  // backward form, preact of x's type
 };
-constexpr int DROP_THREADS = 256, DROP_CHUNKS = 4;  // of 8 elements, per thread
+constexpr int DROP_THREADS = 256;  // 8 elements each
 
 }  // namespace muon
