@@ -41,17 +41,8 @@ __global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const Lin
   const int64_t row = i / eights;
   if (row >= a.m) return;
   const int col = (int)(i - row * eights) * 8, have = min(8, a.n - col);
-  const float* at = a.part + row * a.part_ld + col;  // its rows are padded to whole tiles
-  f32x8 v = load8<GRAD_FP32>(at, 0);
-  for (int s = 1; s < a.splits; s += 4) {  // four loads at a time
-    f32x8 more[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s + k < a.splits) more[k] = load8<GRAD_FP32>(at, (s + k) * a.part_stride);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s + k < a.splits) v += more[k];
-  }
+  // the rows of part are padded to whole tiles
+  const f32x8 v = sum_of_parts(a.part + row * a.part_ld + col, a.part_stride, a.splits);
   const GradEdge store = {a.c, a.ldc, a.add != 0};
   if (have == 8) {
     store.eight(row, col, v);

@@ -134,7 +134,7 @@ struct Slice {
 #pragma unroll
     for (int t = 0; t < LOADS; ++t) {
       uint32_t off = vo[t];
-      if (!KMAJOR && have < BK) {  // have is a multiple of 8
+      if (!KMAJOR && have < BK) {  // the chunk that K ends in holds zeros from there on
         const int slot = (t * NW + wave) * 64 + lane;
         if (swz(slot / CHUNKS, slot % CHUNKS) * 8 >= have) off = 0x80000000u;
       }
@@ -556,7 +556,12 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
   const bool whole = row0 + BM <= a.m && col0 + BN <= a.n;
   if constexpr (!GRAD) {
     const DropKey key(a.e);
-    if (!whole) {
+    if (a.splits > 1) {
+      const int64_t ld = (int64_t)a.tiles_n * BN;
+      float* part = a.part + split * (ld * a.tiles_m * BM);
+      if (whole) store_whole(GradStore<false>(part, ld, row1, col1));
+      else store_edge(GradEdge{part, ld, false});
+    } else if (!whole) {
       store_edge(LayerEdge<TYPE>{a.e, key});
     } else {
       auto with_act = [&](auto backward, auto res) {

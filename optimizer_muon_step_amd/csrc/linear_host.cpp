@@ -140,7 +140,9 @@ double tiles_us(int tile, int64_t tiles, double slices) {
 }
 
 // A split leaves its sums in memory and a last pass adds them up: 3 us for the
-// launch, and the sums written and read at 5 TB/s.
+// launch, and the sums written and read at 5 TB/s.  For a layer of few rows (us, with and
+// without splits): 1 x 768 over 3072 7.3 and 12.7, 64 x 1600 over 6400 11.8 and
+// 20.9, 2048 x 1600 over 6400 57 and 70; 1 x 2304 over 768 is not split, 5.9.
 double splits_us(int64_t m, int64_t n, int64_t splits) { return splits == 1 ? 0 : 3.0 + (double)(m * n * splits) * 8 / 5e6; }
 
 // Tiles, slices and splits of a product: what the measured times make the
@@ -163,7 +165,7 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
     const LinTileSize t = kLinTile[tile];
     const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn, tiles = tm * tn;
     const int slices = ceil_div(k, t.bk);
-    for (int fill = 0; fill <= (grad ? 2 : 0); ++fill) {  // no splits, or as many as make one or two rounds
+    for (int fill = 0; fill <= 2; ++fill) {  // no splits, or as many as make one or two rounds
       const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, slices * t.bk / 256);
       if (fill > 0 && want < 2) continue;
       const int per = slices ? ceil_div(slices, want) : 0, splits = slices ? ceil_div(slices, per) : 1;
@@ -258,6 +260,19 @@ int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool size
   // past the caches: 32768 x 6400 y and z over 1600 712 us so and 755 us through
   // them; 16384 x 3072 over 768, which does stay, 105 and 102.
   e.stream = l->m * out * ((l->y_type == MUON_FP32 ? 4 : 2) + (l->preact && !backward ? 2 : 0)) > ((int64_t)256 << 20);
+  if (g.splits > 1) {
+    const LinTileSize t = kLinTile[p->tile];
+    LinJoinArgs& j = p->join;
+    p->finish = true;
+    j.part_ld = (int64_t)g.tiles_n * t.bn;
+    j.part_stride = j.part_ld * g.tiles_m * t.bm;
+    g.part = (float*)take(p, workspace, (size_t)(j.part_stride * g.splits * 4));
+    j.part = g.part;
+    j.m = g.m;
+    j.n = g.n;
+    j.splits = g.splits;
+    j.e = e;
+  }
   return MUON_OK;
 }
 

@@ -21,8 +21,9 @@ struct LinPlan {
   int tile;
   LinPackArgs pack;  // n of 0: nothing to copy
   LinGemmArgs gemm;
-  bool finish;
-  LinFinishArgs fin;
+  bool finish;         // K was split: a last pass adds the sums up, by
+  LinFinishArgs fin;   // of a weight gradient
+  LinJoinArgs join;    // of a layer
   size_t workspace;  // bytes; with a null workspace the pointers into it are offsets
 };
 

@@ -73,13 +73,12 @@ struct LinGemmArgs {
   int32_t m, n, k;
   int32_t tiles_m, tiles_n;
   int32_t slices;     // of K, of the tile's bk
-  int32_t splits;     // of the slices; above 1 every split leaves its sums in part
+  int32_t splits;     // of the slices; above 1 every split leaves its sums in part, split by split of (tiles_m BM) x (tiles_n BN)
   int32_t per_split;  // slices of a split
   LinEpilogue e;      // of the products of a layer
   // Of a weight gradient: C to c, or added to it; sums of the rows of dz (the B
   // operand's columns where sum_side is 1, the A operand's where it is 2) to
-  // sums.  With splits, part holds splits x (tiles_m BM) x (tiles_n BN) sums and
-  // sum_part splits x (the other side's tiles) x (sum_side's tiles x edge).
+  // sums; with splits, sum_part holds splits x (the other side's tiles) x (sum_side's tiles x edge).
   float* c;
   float* sums;
   float* part;
@@ -105,6 +104,15 @@ struct LinFinishArgs {
   int32_t sum_first_block;               // blocks from here on take the sums
 };
 constexpr int FINISH_THREADS = 256;
+
+// A layer's output from the sums of its splits.
+struct LinJoinArgs {
+  LinEpilogue e;
+  const float* part;
+  int64_t part_ld, part_stride;
+  int32_t m, n, splits;
+};
+static_assert(sizeof(LinJoinArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // Output tiles of the product kernels (see kernels_linear.hip and linear_host.cpp).
 // 64_DEEP has the ring of two compute units' share of 64.

@@ -47,6 +47,7 @@ hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s);
 // dropout: one launch each.
 hipError_t launch_linear(const LinGemmArgs& a, int type, bool b_kmajor, int tile, hipStream_t s);
 hipError_t launch_linear_dw(const LinGemmArgs& a, int type, int tile, hipStream_t s);
+hipError_t launch_linear_join(const LinJoinArgs& a, int type, hipStream_t s);
 hipError_t launch_linear_finish(const LinFinishArgs& a, hipStream_t s);
 hipError_t launch_linear_pack(const LinPackArgs& a, hipStream_t s);
 hipError_t launch_dropout(const DropArgs& a, int64_t blocks, hipStream_t s);

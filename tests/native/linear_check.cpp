@@ -97,6 +97,15 @@ static void check_layers() {
             end = (uintptr_t)c.dst + (size_t)(c.rows * c.dst_ld * 2);
           }
           CHECK(end <= (uintptr_t)at(512) + p.workspace && p.workspace % 256 == 0);
+          CHECK(p.finish == (p.gemm.splits > 1));
+          if (p.finish) {  // the sums of the splits lie behind the copies
+            const LinTileSize t = kLinTile[p.tile];
+            const LinJoinArgs& j = p.join;
+            CHECK(j.m == m && j.n == out && j.splits == p.gemm.splits && j.part == p.gemm.part && (uintptr_t)j.part >= end);
+            CHECK(j.part_ld == (int64_t)p.gemm.tiles_n * t.bn && j.part_stride == j.part_ld * p.gemm.tiles_m * t.bm);
+            CHECK((const char*)(j.part + j.part_stride * j.splits) <= (const char*)at(512) + p.workspace);
+            CHECK(j.e.y == l.y && j.e.ldy == l.ldy && j.e.backward == backward && j.e.act == l.act);
+          }
           CHECK(p.b_kmajor == (backward == (l.w_transposed != 0)));
         }
   CHECK(tiles.size() == LIN_TILES);
@@ -109,6 +118,14 @@ static void check_layers() {
   CHECK(run(layer(2000, 200, 1100), false, &p) == MUON_OK && p.tile == LIN_TILE_128);
   CHECK(run(layer(4097, 72, 2311), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
   CHECK(run(layer(4160, 136, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
+  // and with its reduction split
+  const struct {
+    int64_t m, k, n;
+    int tile;
+  } splits[] = {{1, 4096, 72, LIN_TILE_64}, {64, 6400, 1600, LIN_TILE_64_DEEP}, {130, 9000, 200, LIN_TILE_32},
+                {520, 20000, 1000, LIN_TILE_128}, {2048, 20000, 1032, LIN_TILE_256}};
+  for (const auto& s : splits) CHECK(run(layer(s.m, s.k, s.n), false, &p) == MUON_OK && p.finish && p.tile == s.tile);
+  CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && !p.finish);
   // a matrix that is readable but for one thing
   muon_linear_t l = layer(64, 64, 64);
   CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 0 && p.workspace == 0);

@@ -113,6 +113,64 @@ def test_linear_epilogues(act, parts, out, kind, w_kind, shape):
                  "keep" in parts)
 
 
+# few tiles and a long reduction, which is split: 64 x 64 tiles with either ring, 32 x 64, 128 x 128 and 256 x 256
+SPLIT = [(1, 4096, 72), (64, 6400, 1600), (9, 20001, 31), (257, 30000, 513), (130, 9000, 200), (520, 20000, 1000), (2048, 20000, 1032)]
+
+
+@pytest.mark.parametrize("order", ["rows", "columns"])
+@pytest.mark.parametrize("shape", SPLIT, ids=str)
+def test_split_reductions(shape, order):
+    import optimizer_muon_step_amd as mu
+    m, k, n = shape
+    rng = np.random.default_rng(m + k * 3 + n)
+    say(f"[linear, dx] {shape} {order}")
+    x, w = make(rng, (m, k), "bf16"), make(rng, (k, n), "bf16", 0.1, order=order)
+    check_linear(mu, x, w, "bf16", bias=make(rng, (1, n), "fp32")[0], act="gelu", drop=(0.2, 1, 2, 3), keep=True)
+    dz, w = make(rng, (m, k), "fp16", 0.1), make(rng, (n, k), "fp16", 0.1, order=order)
+    check_dx(mu, dz, w, "fp16", out="fp32", residual=make(rng, (m, n), "fp32"))
+
+
+@pytest.mark.parametrize("act", [None, "gelu", "relu", "relu2"])
+@pytest.mark.parametrize("parts", ["", "bias", "residual", "drop", "bias residual drop keep"])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("kind,w_kind,shape", [("bf16", "fp32", (33, 2001, 67)), ("fp16", "fp16", (1, 4096, 136))])
+def test_split_epilogues(act, parts, out, kind, w_kind, shape):
+    """Forward with a bias, dx without one."""
+    import optimizer_muon_step_amd as mu
+    m, k, n = shape
+    rng = np.random.default_rng(7)
+    x, w = make(rng, (m, k), kind), make(rng, (k, n), w_kind, 0.1)
+    res = make(rng, (m, n), kind if out == "same" else out) if "residual" in parts else None
+    bias = make(rng, (1, n), "fp32")[0] if "bias" in parts else None
+    drop = (0.3, 0x123456789ABCDEF0, 77, 5) if "drop" in parts else None
+    check_linear(mu, x, w, kind, out, bias, act, drop, res, "keep" in parts)
+    pre = None if act is None else make(rng, (m, n), kind, 2.0)
+    check_dx(mu, x, w.T, kind, out=out, act=act, preact=pre, residual=res, drop=drop)
+
+
+def test_split_in_place_and_captured():
+    """Two captured calls whose reductions are split, the output the residual, replayed among eager calls."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    rng = np.random.default_rng(8)
+    x, w = make(rng, (33, 4100), "bf16"), make(rng, (4100, 4100), "bf16", 0.02)
+    y, start = make(rng, (33, 4100), "bf16"), make(rng, (33, 4100), "bf16")
+    for _ in range(2):
+        mu.muon_linear(x, w, residual=y, out=y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mu.muon_linear(x, w, residual=y, out=y)
+        mu.muon_linear(y, w, residual=y, act="relu", preact=(z := torch.empty_like(y)), out=(out := torch.empty_like(y)))
+    for _ in range(3):
+        y.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = mu.muon_linear(x, w, residual=start)
+        want_z = torch.empty_like(y)
+        assert torch.equal(out, mu.muon_linear(want, w, residual=want, act="relu", preact=want_z))
+        assert torch.equal(y, want) and torch.equal(z, want_z)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("order", ["rows", "columns"])
 @pytest.mark.parametrize("m,k,n,gap,offset", [(40, 72, 88, 56, 0), (130, 72, 200, 8, 0), (129, 136, 136, 64, 8),
