@@ -339,9 +339,11 @@ int muon_step_clip(float* const* params, const float* const* grads, float* const
  *             ldr, ldy, ldp elements apart, any alignment of the element
  *             type.  w_transposed = 1: w is stored n x k (ldw from row to row of k).
  *             Rows that are read may overlap (a distance of 0 repeats one); rows that are
- *             written may not.  A matrix whose base is not 16-byte aligned, whose
- *             rows are not a multiple of 8 elements apart or long, or
- *             which is fp32 is copied to the workspace first: x costs that pass once more.
+ *             written may not.  The fastest kernels read matrices
+ *             whose base is 16-byte aligned and whose rows are a multiple of 8
+ *             elements apart (at most MUON_LINEAR_MAX_WIDTH) and long.  Others, and fp32
+ *             weights, are read through registers by small products and copied to the workspace
+ *             first by large ones: x costs that pass once more.
  *   x_type    MUON_BF16 or MUON_FP16, also the type of preact
  *   w_type, bias_type   x_type or MUON_FP32
  *   y_type    x_type or MUON_FP32, also the type of residual
@@ -414,7 +416,8 @@ size_t muon_linear_dw_workspace_bytes(const muon_linear_dw_t* layer);
  * the fields and the rules of muon_linear_t.  Without preact this is dropout and
  * its gradient (the same call on dy); with it, the gradient dz of a layer's z.
  * x_type any of the three types, also that of preact; y_type any, also that of
- * residual; n up to MUON_DROPOUT_MAX_COLS.  y may be x, preact or residual itself.
+ * residual; n up to MUON_DROPOUT_MAX_COLS, and up to about 2^35 elements in all (2^24 blocks
+ * of 256 groups of 8).  y may be x, preact or residual itself.
  */
 #define MUON_DROPOUT_MAX_COLS ((int64_t)1 << 34)
 typedef struct {

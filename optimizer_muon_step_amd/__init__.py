@@ -408,9 +408,9 @@ def muon_linear(x, w, bias=None, act=None, dropout=0.0, rng=None, site=0, residu
     `residual` and the result are of x's type or float32 (`out_dtype`; by default the
     residual's type, or x's); `out` is a tensor to fill, and may be the residual.
     `preact`, of x's type, receives x w + bias for the backward pass.  Rows may
-    lie apart in memory and start anywhere; the kernels read them in place if rows
-    are 16-byte aligned and multiples of 8 elements long, and through a copy
-    otherwise.  `stream` as in muon_grad_norm.  No autograd graph is recorded."""
+    lie apart in memory and start anywhere; the fastest kernels take rows
+    that are 16-byte aligned and multiples of 8 elements long, and large products copy
+    others (and float32 weights) first.  `stream` as in muon_grad_norm.  No autograd graph is recorded."""
     return _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preact, 0, stream)
 
 

@@ -16,6 +16,7 @@ static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
     case LIN_TILE_256: linear_gemm_kernel<TYPE, true, true, true, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_128: linear_gemm_kernel<TYPE, true, true, true, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 128, 2, 2, 2, 2, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_64_ANY: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 128, 2, 2, 2, 2, 2, READ_ANY><<<grid, threads, 0, s>>>(a); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -25,14 +26,28 @@ hipError_t launch_linear_dw(const LinGemmArgs& a, int type, int tile, hipStream_
   return type == GRAD_BF16 ? launch_tile<GRAD_BF16>(a, tile, s) : launch_tile<GRAD_FP16>(a, tile, s);
 }
 
-// A thread to eight elements of a row of c, and behind them a thread to each
-// sum.  The splits are added in their order, so equal calls give equal bits.
+// A thread to eight elements of a row of c, and behind them a block to 32 of the
+// sums, whose many rows its 8 groups of threads share.  Everything is added in an order
+// that the sizes give, so equal calls give equal bits.
 __global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const LinFinishArgs a) {
   if ((int)blockIdx.x >= a.sum_first_block) {
-    const int i = ((int)blockIdx.x - a.sum_first_block) * FINISH_THREADS + threadIdx.x;
-    if (i >= a.n_sums) return;
+    constexpr int GROUPS = FINISH_THREADS / FINISH_SUMS;
+    __shared__ float of_group[GROUPS][FINISH_SUMS];
+    const int lane = threadIdx.x % FINISH_SUMS, group = threadIdx.x / FINISH_SUMS;
+    const int i = ((int)blockIdx.x - a.sum_first_block) * FINISH_SUMS + lane;
+    const MUON_GLOBAL float* p = gptr(a.sum_part) + min(i, a.n_sums - 1);
     float v = 0.0f;
-    for (int r = 0; r < a.sum_rows; ++r) v += gptr(a.sum_part)[r * a.sum_stride + i];
+    for (int r = group; r < a.sum_rows; r += 4 * GROUPS) {
+      float more[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) more[k] = r + k * GROUPS < a.sum_rows ? p[(r + k * GROUPS) * a.sum_stride] : 0.0f;
+      v += (more[0] + more[1]) + (more[2] + more[3]);
+    }
+    of_group[group][lane] = v;
+    __syncthreads();
+    if (group != 0 || i >= a.n_sums) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) v += of_group[g][lane];
     gptr(a.sums)[i] = a.add ? gptr(a.sums)[i] + v : v;
     return;
   }
@@ -54,7 +69,7 @@ __global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const Lin
 }
 
 hipError_t launch_linear_finish(const LinFinishArgs& a, hipStream_t s) {
-  const int blocks = a.sum_first_block + (a.n_sums + FINISH_THREADS - 1) / FINISH_THREADS;
+  const int blocks = a.sum_first_block + (a.n_sums + FINISH_SUMS - 1) / FINISH_SUMS;
   linear_finish_kernel<<<blocks, FINISH_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }

@@ -25,7 +25,7 @@ int enqueue_layer(const muon_linear_t* l, bool backward, void* workspace, size_t
   if (rc || p.empty) return rc;
   std::lock_guard<std::mutex> lock(api_mutex());
   if ((rc = enqueue_pack(p, MUON_KERNEL_LINEAR, stream))) return rc;
-  rc = timed(MUON_KERNEL_LINEAR, stream, [&] { return launch_linear(p.gemm, p.type, p.b_kmajor, p.tile, stream); },
+  rc = timed(MUON_KERNEL_LINEAR, stream, [&] { return launch_linear(p.gemm, p.type, p.b_kmajor, p.b_wide, p.tile, stream); },
              "layer product kernel launch");
   if (rc || !p.finish) return rc;
   return timed(MUON_KERNEL_LINEAR, stream, [&] { return launch_linear_join(p.join, p.type, stream); },

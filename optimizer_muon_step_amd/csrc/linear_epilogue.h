@@ -67,16 +67,16 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
   return grad::Elem<TYPE>::widen1(gptr(static_cast<const typename grad::Elem<TYPE>::scalar*>(p))[i]);
 }
 
-// The sum of eights `stride` apart, in their order; four loads at a time.
+// The sum of eights `stride` apart, in their order; eight loads at a time.
 __device__ __forceinline__ f32x8 sum_of_parts(const float* at, int64_t stride, int parts) {
   f32x8 v = load8<GRAD_FP32>(at, 0);
-  for (int s = 1; s < parts; s += 4) {
-    f32x8 more[4];
+  for (int s = 1; s < parts; s += 8) {
+    f32x8 more[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
       if (s + k < parts) more[k] = load8<GRAD_FP32>(at, (s + k) * stride);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
       if (s + k < parts) v += more[k];
   }
   return v;

@@ -171,6 +171,118 @@ struct Slice {
   }
 };
 
+// The same slice through registers, of an operand that buffer loads to LDS cannot
+// read: rows that start at any element, of any length from 8 on, of 16 or (WIDE)
+// 32 bits, the latter rounded to TYPE on the way.  Every load is of 8 elements within the operand: a chunk
+// that its row ends in is read from 8 before the row's end on and moved down, one
+// outside is read elsewhere.  What lies behind K becomes zeros; rows and columns that
+// the tile hangs over hold something, which the output's bounds leave out.  A slice of 128 takes
+// about 1.2 times as long as by direct loads, 1.7 times where rows start off 16 bytes; what it saves
+// is the copy's launch and its pass (linear_host.cpp weighs them).
+template <int TYPE, bool WIDE, bool KMAJOR, int R, int NW, int BK>
+struct AnySlice : Slice<KMAJOR, R, NW, BK> {
+  typedef Slice<KMAJOR, R, NW, BK> Base;
+  using Base::CHUNKS;
+  using Base::LOADS;
+  using Base::swz;
+  static constexpr int SIZE = WIDE ? 4 : 2;
+  struct Held {
+    u32x4 lo[LOADS], hi[WIDE ? LOADS : 1];
+  };
+
+  const char* base;
+  int64_t ld;        // bytes
+  int rows, cols;    // as stored
+  int first;
+  int64_t at[LOADS];  // k-contiguous: of this lane's row; k-major: of its columns
+  int place[LOADS];   // k-contiguous: the chunk's first column; k-major: its row in a slice
+  int down[LOADS];    // k-major: elements to move down
+
+  __device__ __forceinline__ void start(const LinOperand& o, int first_, int side, int k, int wave, int lane) {
+    base = (const char*)o.p;
+    ld = o.ld;
+    first = first_;
+    rows = KMAJOR ? k : side;
+    cols = KMAJOR ? side : k;
+#pragma unroll
+    for (int t = 0; t < LOADS; ++t) {
+      const int slot = (t * NW + wave) * 64 + lane, row = slot / CHUNKS, col = swz(row, slot % CHUNKS) * 8;
+      if (KMAJOR) {
+        const int from = min(first + col, cols - 8);
+        at[t] = (int64_t)from * SIZE;
+        down[t] = first + col - from;
+        place[t] = row;
+      } else {
+        at[t] = min(first + row, rows - 1) * ld;
+        place[t] = col;
+      }
+    }
+  }
+
+  // Slice s of K.
+  __device__ __forceinline__ void fetch(Held& h, int s) const {
+#pragma unroll
+    for (int t = 0; t < LOADS; ++t) {
+      const int p = s * BK + place[t];
+      int64_t off;
+      if (KMAJOR) off = at[t] + min(p, rows - 1) * ld;
+      else off = at[t] + (int64_t)(p + 8 <= cols ? p : p < cols ? cols - 8 : 0) * SIZE;
+      const char* from = base + off;
+      if (WIDE) {
+        h.lo[t] = __builtin_bit_cast(u32x4, load_raw4(from));
+        h.hi[t] = __builtin_bit_cast(u32x4, load_raw4(from + 16));
+      } else {
+        h.lo[t] = load_raw<GRAD_BF16>(from, 0);
+      }
+    }
+  }
+  static __device__ __forceinline__ f32x4 load_raw4(const char* p) {
+    const f32x4_u w = *reinterpret_cast<const MUON_GLOBAL f32x4_u*>(gptr(reinterpret_cast<const float*>(p)));
+    return f32x4{w.x, w.y, w.z, w.w};
+  }
+
+  // What was fetched of slice s to LDS at `to`.
+  __device__ __forceinline__ void put(LIN_LDS char* to, const Held& h, int s, int wave, int lane) const {
+    const bool k_ends = (s + 1) * BK > (KMAJOR ? rows : cols), hangs = KMAJOR && first + R > cols;
+#pragma unroll
+    for (int t = 0; t < LOADS; ++t) {
+      u32x4 lo = h.lo[t], hi;
+      if (WIDE) hi = h.hi[t];
+      if (k_ends || hangs) {  // uniform
+        const int p = s * BK + place[t];
+        const int by = KMAJOR ? down[t] : max(0, p + 8 - cols);
+        if (by < 8) {
+          move_down(lo, hi, by);
+        } else {
+          lo = 0;
+          if (WIDE) hi = 0;
+        }
+        if (KMAJOR && p >= rows) {
+          lo = 0;
+          if (WIDE) hi = 0;
+        }
+      }
+      if (WIDE) {
+        const f32x4 a = __builtin_bit_cast(f32x4, lo), b = __builtin_bit_cast(f32x4, hi);
+        lo = narrow8<TYPE>(f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+      }
+      *(LIN_LDS u32x4*)(to + ((t * NW + wave) * 64 + lane) * 16) = lo;
+    }
+  }
+  // Elements `by` .. 7 to 0 .., zeros behind them.
+  static __device__ __forceinline__ void move_down(u32x4& lo, u32x4& hi, int by) {
+    if constexpr (WIDE) {
+      if (by & 4) lo = hi, hi = 0;
+      if (by & 2) lo = u32x4{lo.z, lo.w, hi.x, hi.y}, hi = u32x4{hi.z, hi.w, 0, 0};
+      if (by & 1) lo = u32x4{lo.y, lo.z, lo.w, hi.x}, hi = u32x4{hi.y, hi.z, hi.w, 0};
+    } else {
+      if (by & 4) lo = u32x4{lo.z, lo.w, 0, 0};
+      if (by & 2) lo = u32x4{lo.y, lo.z, lo.w, 0};
+      if (by & 1) lo = u32x4{lo.x >> 16 | lo.y << 16, lo.y >> 16 | lo.z << 16, lo.z >> 16 | lo.w << 16, lo.w >> 16};
+    }
+  }
+};
+
 template <int TYPE>
 __device__ __forceinline__ float fragment_sum(s16x8 f) {
   const f32x8 v = widen8<TYPE>(__builtin_bit_cast(u32x4, f));
@@ -310,14 +422,18 @@ struct GradEdge {
   }
 };
 
+// How the operands reach LDS: by buffer loads; through registers; so, and B is fp32.
+enum LinRead { READ_DIRECT = 0, READ_ANY = 1, READ_ANY_WIDE = 2 };
+
 // BLOCKS: blocks a compute unit is to hold.
-template <int TYPE, bool AK, bool BKM, bool GRAD, int BM, int BN, int BK, int WM, int WN, int WK, int NSTAGE, int BLOCKS>
+template <int TYPE, bool AK, bool BKM, bool GRAD, int BM, int BN, int BK, int WM, int WN, int WK, int NSTAGE, int BLOCKS, int READ = READ_DIRECT>
 __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void linear_gemm_kernel(const LinGemmArgs a) {
   constexpr int NW = WM * WN * WK;
   constexpr int WTM = BM / WM, WTN = BN / WN;  // wave tile
   constexpr int TM = WTM / 16, TN = WTN / 16, PARTS = WTM / 32;
-  typedef Slice<AK, BM, NW, BK> SA;
-  typedef Slice<BKM, BN, NW, BK> SB;
+  typedef typename std::conditional<READ == READ_DIRECT, Slice<AK, BM, NW, BK>, AnySlice<TYPE, false, AK, BM, NW, BK>>::type SA;
+  typedef typename std::conditional<READ == READ_DIRECT, Slice<BKM, BN, NW, BK>,
+                                    AnySlice<TYPE, READ == READ_ANY_WIDE, BKM, BN, NW, BK>>::type SB;
   constexpr int STAGE = SA::BYTES + SB::BYTES;
   constexpr int PER = SA::LOADS + SB::LOADS;
   constexpr int STEPS = BK / 32 / WK;  // k-steps of a wave in a slice
@@ -350,17 +466,24 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
 
   SA la;
   SB lb;
-  la.start(a.a, row0, s0, wave, lane);
-  lb.start(a.b, col0, s0, wave, lane);
   auto stage_of = [&](int s) { return (LIN_LDS char*)lds + (s % NSTAGE) * STAGE; };
   auto issue = [&](int s) {
-    const int have = a.k - (s0 + s) * BK;
-    la.load(stage_of(s), have, wave, lane);
-    lb.load(stage_of(s) + SA::BYTES, have, wave, lane);
+    if constexpr (READ == READ_DIRECT) {
+      const int have = a.k - (s0 + s) * BK;
+      la.load(stage_of(s), have, wave, lane);
+      lb.load(stage_of(s) + SA::BYTES, have, wave, lane);
+    }
   };
+  if constexpr (READ == READ_DIRECT) {
+    la.start(a.a, row0, s0, wave, lane);
+    lb.start(a.b, col0, s0, wave, lane);
 #pragma unroll
-  for (int s = 0; s < NSTAGE; ++s)
-    if (s < slices) issue(s);
+    for (int s = 0; s < NSTAGE; ++s)
+      if (s < slices) issue(s);
+  } else {
+    la.start(a.a, row0, a.m, a.k, wave, lane);
+    lb.start(a.b, col0, a.n, a.k, wave, lane);
+  }
 
   typename SA::Read ra[TM];
   typename SB::Read rb[TN];
@@ -399,6 +522,22 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma<TYPE>(fb[set][j], fa[set][i], acc[i][j]);
   };
 
+  auto add_sums = [&](int s) {
+    if (!summing || (sharers != 1 && (s0 + s) % sharers != across)) return;
+    const LIN_LDS char* sa = stage_of(s);
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int kk = WK == 1 ? t : t * WK + wk;
+      if (a.sum_side == 1) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sum[j] += fragment_sum<TYPE>(SB::fragment(sa + SA::BYTES, rb[j], kk));
+      } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sum[i] += fragment_sum<TYPE>(SA::fragment(sa, ra[i], kk));
+      }
+    }
+  };
+
   // Slice s is there once this wave has only the loads of later slices
   // outstanding and every wave has passed a barrier.
   auto reduce = [&](auto works) {
@@ -410,20 +549,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
 #pragma unroll 1
     for (int s = 0; s < slices; ++s) {
       if constexpr (GRAD && WORKS) {
-        if (summing && (sharers == 1 || (s0 + s) % sharers == across)) {
-          const LIN_LDS char* sa = stage_of(s);
-#pragma unroll
-          for (int t = 0; t < STEPS; ++t) {
-            const int kk = WK == 1 ? t : t * WK + wk;
-            if (a.sum_side == 1) {
-#pragma unroll
-              for (int j = 0; j < TN; ++j) sum[j] += fragment_sum<TYPE>(SB::fragment(sa + SA::BYTES, rb[j], kk));
-            } else {
-#pragma unroll
-              for (int i = 0; i < TM; ++i) sum[i] += fragment_sum<TYPE>(SA::fragment(sa, ra[i], kk));
-            }
-          }
-        }
+        add_sums(s);
       }
       if constexpr (WORKS && READS_AHEAD) {
 #pragma unroll
@@ -451,9 +577,59 @@ __global__ __launch_bounds__(64 * WM * WN * WK, WM * WN * WK * BLOCKS / 4) void 
       }
     }
   };
+  // Through registers: two LDS buffers, and two slices more on their way in registers.
+  auto reduce_any = [&](auto works) {
+    constexpr bool WORKS = decltype(works)::value;
+    if constexpr (READ != READ_DIRECT) {
+      static_assert(NSTAGE == 2, "one buffer is filled while the other is read");
+      if (slices == 0) return;
+      typename SA::Held ha[2];
+      typename SB::Held hb[2];
+      // behind the last slice, that one again: loads without a branch can be waited for one by one
+      auto fetch = [&](int s, int set) __attribute__((always_inline)) {
+        la.fetch(ha[set], s0 + min(s, slices - 1));
+        lb.fetch(hb[set], s0 + min(s, slices - 1));
+      };
+      auto put = [&](int s, int set) __attribute__((always_inline)) {
+        la.put(stage_of(set), ha[set], s0 + s, wave, lane);
+        lb.put(stage_of(set) + SA::BYTES, hb[set], s0 + s, wave, lane);
+      };
+      auto step = [&](int s, int set) __attribute__((always_inline)) {
+        // slice s is in LDS, and every wave has read all of the one before
+        wait_loads<63>();
+        block_barrier();
+        if (s + 1 < slices) put(s + 1, set ^ 1);
+        fetch(s + 3, set ^ 1);
+        if constexpr (GRAD && WORKS) add_sums(s);
+        if constexpr (WORKS) {
+#pragma unroll
+          for (int t = 0; t < STEPS; ++t) {
+            read(s, t, 0);
+            multiply(0);
+          }
+        }
+      };
+      fetch(0, 0);
+      fetch(1, 1);
+      put(0, 0);
+      fetch(2, 0);
+      for (int s = 0;; s += 2) {
+        step(s, 0);
+        if (s + 1 >= slices) break;
+        step(s + 1, 1);
+        if (s + 2 >= slices) break;
+      }
+    }
+  };
   // A wave whose part of the tile lies outside the output only helps to load.
-  if (row0 + wi * WTM >= a.m || col0 + wj * WTN >= a.n) reduce(std::false_type{});
-  else reduce(std::true_type{});
+  const bool outside = row0 + wi * WTM >= a.m || col0 + wj * WTN >= a.n;
+  if constexpr (READ != READ_DIRECT) {
+    if (outside) reduce_any(std::false_type{});
+    else reduce_any(std::true_type{});
+  } else {
+    if (outside) reduce(std::false_type{});
+    else reduce(std::true_type{});
+  }
   wait_loads<0>();
   block_barrier();
 

@@ -106,6 +106,7 @@ char* take(LinPlan* p, void* workspace, size_t bytes) {
 
 // The operand that the kernels read for m, through a copy where they must.
 LinOperand operand_of(const Matrix& m, int type, LinPlan* plan, void* workspace) {
+  if (plan->tile == LIN_TILE_64_ANY) return {m.p, m.ld * (int64_t)m.size(), 0};
   if (readable(m, type)) {
     const int64_t ld = m.rows == 1 ? m.cols : m.ld;
     return {m.p, ld * 2, ((m.rows - 1) * ld + m.cols) * 2};
@@ -123,13 +124,15 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // that small tiles leave room for.  Over a K of 768 a round of 256 x 256 tiles
 // takes 26.6, of 128 x 128 13.2 and 19, of 64 x 64 6.2 and 8.8, of 32 x 64 5.3 and
 // 6.9; over 3072 77, 35 and 49, 14 and 22, 12 and 16.  Two k-major operands (a weight
-// gradient's) take 1.17 of that a slice.
+// gradient's) take 1.17 of that a slice, and rows that do not start at
+// multiples of 16 bytes, loaded through registers, 1.45.
 struct TileCost {
   double one, one_slice, two, two_slice;  // two = 0: no second tile fits
 };
 constexpr TileCost kTileCost[LIN_TILES] = {
-    {9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24}};
-constexpr double GRAD_SLICE = 1.17;
+    {9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24},
+    {4.0, 0.27, 5.0, 0.46}};
+constexpr double GRAD_SLICE = 1.17, UNALIGNED_SLICE = 1.45;
 
 double tiles_us(int tile, int64_t tiles, double slices) {
   const TileCost& c = kTileCost[tile];
@@ -145,12 +148,34 @@ double tiles_us(int tile, int64_t tiles, double slices) {
 // 20.9, 2048 x 1600 over 6400 57 and 70; 1 x 2304 over 768 is not split, 5.9.
 double splits_us(int64_t m, int64_t n, int64_t splits) { return splits == 1 ? 0 : 3.0 + (double)(m * n * splits) * 8 / 5e6; }
 
+// The copies that operands need in all tiles but 64_ANY: 3 us for the launch, their
+// bytes at 4 TB/s.
+struct Copies {
+  double us = 0;
+  bool avoidable = false;  // there are some, and 64_ANY can do without
+  bool unaligned = false;
+  Copies(const Matrix& a, const Matrix& b, int type) {
+    for (const Matrix* m : {&a, &b}) {
+      if (m->rows == 0) return;
+      if (!readable(*m, type)) us += (double)(m->rows * m->cols) * (double)(m->size() + 2) / 4e6;
+      unaligned = unaligned || m->lo() % 16 != 0 || m->ld * (int64_t)m->size() % 16 != 0;
+    }
+    if (us == 0) return;
+    us += 3.0;
+    avoidable = a.cols >= 8 && b.cols >= 8;
+  }
+};
+
 // Tiles, slices and splits of a product: what the measured times make the
 // fastest.  Examples (us, chosen and next): 16384 x 3072 over 768 82 in 256 x 256
 // tiles, 90 in 128 x 128; 8192 x 2304 over 768 43 in 128 x 128, 55 in 256 x 256;
 // 1024 x 768 over 2304 11.4 in 64 x 64 with the deep ring, 12.6 with the other, 28
 // in 128 x 128; 512 x 768 over 3072 12.2 in 32 x 64, 13.4 in 64 x 64.
-int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
+//
+// 64_ANY stands against the copies and any other tile: 1 x 2304 over 768 of an fp32 weight
+// 6.8 us in it and 9.6 with the copy, 1999 x 771 over 1001 16.3 and 18.8; 4096 x 768
+// over 768 of an fp32 weight 17.0 and 16.1, 16384 x 3072 235 and 99.
+int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies& copies) {
   LinGemmArgs& g = p->gemm;
   g.m = (int32_t)m;
   g.n = (int32_t)n;
@@ -159,9 +184,12 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
   for (int tile = 0; tile < LIN_TILES; ++tile) {
     // few rows of a weight, or few weights over few rows, are no case worth a kernel
     if (grad && (tile == LIN_TILE_32 || tile == LIN_TILE_64_DEEP)) continue;
+    if (tile == LIN_TILE_64_ANY && !copies.avoidable) continue;
     // up to 32 rows it makes no more tiles, and each loads with fewer waves: one row of
     // 2304 over 768 7.5 us, 5.5 in 64 x 64
     if (tile == LIN_TILE_32 && m <= 32) continue;
+    const bool any = tile == LIN_TILE_64_ANY;
+    const double slower = (grad ? GRAD_SLICE : 1.0) * (any && copies.unaligned ? UNALIGNED_SLICE : 1.0);
     const LinTileSize t = kLinTile[tile];
     const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn, tiles = tm * tn;
     const int slices = ceil_div(k, t.bk);
@@ -169,7 +197,7 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad) {
       const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, slices * t.bk / 256);
       if (fill > 0 && want < 2) continue;
       const int per = slices ? ceil_div(slices, want) : 0, splits = slices ? ceil_div(slices, per) : 1;
-      const double us = tiles_us(tile, tiles * splits, per * t.bk / 64.0 * (grad ? GRAD_SLICE : 1.0)) + splits_us(m, n, splits);
+      const double us = tiles_us(tile, tiles * splits, per * t.bk / 64.0 * slower) + splits_us(m, n, splits) + (any ? 0 : copies.us);
       if (best != 0 && us >= best) continue;
       best = us;
       p->tile = tile;
@@ -237,7 +265,8 @@ int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool size
         if (all[i].written && overlap(all[i], rng)) return fail(MUON_EINVAL, "%s overlaps rng", all[i].what);
     }
   }
-  if ((rc = lay_out(p, l->m, out, in, false))) return rc;
+  if ((rc = lay_out(p, l->m, out, in, false, Copies(x, w, type)))) return rc;
+  p->b_wide = p->tile == LIN_TILE_64_ANY && w.type == MUON_FP32;
   LinGemmArgs& g = p->gemm;
   g.a = operand_of(x, type, p, workspace);
   g.b = operand_of(w, type, p, workspace);
@@ -306,7 +335,7 @@ int plan_grad(const muon_linear_dw_t* l, void* workspace, bool sizes_only, LinPl
     if ((rc = check_overlaps(all, none, n))) return rc;
   }
   p->empty = l->m == 0 && l->accumulate;
-  if ((rc = lay_out(p, rows, cols, l->m, true))) return rc;
+  if ((rc = lay_out(p, rows, cols, l->m, true, Copies(x, dz, type)))) return rc;
   LinGemmArgs& g = p->gemm;
   if (l->m > 0) {
     const LinOperand ox = operand_of(x, type, p, workspace), oz = operand_of(dz, type, p, workspace);

@@ -17,6 +17,7 @@ namespace muon {
 struct LinPlan {
   bool empty;      // nothing to compute
   bool b_kmajor;   // of a layer's product (a weight gradient's operands both are)
+  bool b_wide;     // B is read as fp32
   int type;
   int tile;
   LinPackArgs pack;  // n of 0: nothing to copy

@@ -39,7 +39,8 @@ struct LinEpilogue {
 };
 
 // An operand as the products read it: 16-bit elements, 16-byte aligned, rows of
-// a multiple of 8 elements apart, rows of a multiple of 8 elements.
+// a multiple of 8 elements apart, rows of a multiple of 8 elements.  64_ANY tiles read
+// any other too (rows of 8 elements at least, B also fp32), and not by `bytes`.
 struct LinOperand {
   const void* p;
   int64_t ld;     // bytes from row to row
@@ -103,7 +104,7 @@ struct LinFinishArgs {
   int32_t add;
   int32_t sum_first_block;               // blocks from here on take the sums
 };
-constexpr int FINISH_THREADS = 256;
+constexpr int FINISH_THREADS = 256, FINISH_SUMS = 32;  // sums of a block
 
 // A layer's output from the sums of its splits.
 struct LinJoinArgs {
@@ -115,13 +116,13 @@ struct LinJoinArgs {
 static_assert(sizeof(LinJoinArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // Output tiles of the product kernels (see kernels_linear.hip and linear_host.cpp).
-// 64_DEEP has the ring of two compute units' share of 64.
-enum LinTile { LIN_TILE_256 = 0, LIN_TILE_128, LIN_TILE_64, LIN_TILE_64_DEEP, LIN_TILE_32, LIN_TILES };
+// 64_DEEP has the ring of two compute units' share of 64; 64_ANY loads through registers.
+enum LinTile { LIN_TILE_256 = 0, LIN_TILE_128, LIN_TILE_64, LIN_TILE_64_DEEP, LIN_TILE_32, LIN_TILE_64_ANY, LIN_TILES };
 struct LinTileSize {
   int bm, bn, bk, threads;
 };
 constexpr LinTileSize kLinTile[LIN_TILES] = {
-    {256, 256, 64, 512}, {128, 128, 64, 256}, {64, 64, 128, 512}, {64, 64, 128, 512}, {32, 64, 128, 256}};
+    {256, 256, 64, 512}, {128, 128, 64, 256}, {64, 64, 128, 512}, {64, 64, 128, 512}, {32, 64, 128, 256}, {64, 64, 128, 512}};
 
 // Dropout by itself.
 struct DropArgs {

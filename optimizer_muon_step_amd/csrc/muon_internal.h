@@ -43,9 +43,9 @@ hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t s);
 hipError_t launch_adamw_clip(const AdamClipArgs& a, hipStream_t s);
 
 // A layer's products (type: of the operands; b_kmajor: operand B has rows of the
-// reduced index), the copies and the pass over splits that they may need, and
+// reduced index; b_wide: it is fp32), the copies and the pass over splits that they may need, and
 // dropout: one launch each.
-hipError_t launch_linear(const LinGemmArgs& a, int type, bool b_kmajor, int tile, hipStream_t s);
+hipError_t launch_linear(const LinGemmArgs& a, int type, bool b_kmajor, bool b_wide, int tile, hipStream_t s);
 hipError_t launch_linear_dw(const LinGemmArgs& a, int type, int tile, hipStream_t s);
 hipError_t launch_linear_join(const LinJoinArgs& a, int type, hipStream_t s);
 hipError_t launch_linear_finish(const LinFinishArgs& a, hipStream_t s);

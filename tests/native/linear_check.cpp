@@ -66,7 +66,7 @@ static void check_gemm(const LinPlan& p, int64_t m, int64_t n, int64_t k) {
   CHECK((int64_t)g.slices * t.bk >= k && (int64_t)(g.slices - 1) * t.bk < k);
   CHECK(g.splits >= 1 && (int64_t)g.splits * g.per_split >= g.slices && (g.splits - 1) * g.per_split < std::max(1, g.slices));
   for (const LinOperand* o : {&g.a, &g.b}) {
-    if (k == 0) continue;
+    if (k == 0 || p.tile == LIN_TILE_64_ANY) continue;
     CHECK((uintptr_t)o->p % 16 == 0 && o->ld % 16 == 0 && o->ld < ((int64_t)1 << 24) && o->bytes % 16 == 0);
     CHECK(255 * o->ld + 128 < 0x7ffffff0);  // a tile's offsets
   }
@@ -87,8 +87,14 @@ static void check_layers() {
           check_gemm(p, m, out, in);
           tiles.insert(p.tile);
           const bool x_copied = in % 8 != 0, w_copied = (v & 4) || (l.w_transposed ? k : n) % 8 != 0;
-          CHECK(p.pack.n == x_copied + w_copied);
-          CHECK((p.gemm.a.p == l.x) == !x_copied && (p.gemm.b.p == l.w) == !w_copied);
+          if (p.tile == LIN_TILE_64_ANY) {
+            CHECK((x_copied || w_copied) && in >= 8 && (l.w_transposed ? k : n) >= 8 && p.b_wide == ((v & 4) != 0));
+            CHECK(p.pack.n == 0 && p.gemm.a.p == l.x && p.gemm.b.p == l.w);
+            CHECK(p.gemm.a.ld == l.ldx * 2 && p.gemm.b.ld == l.ldw * (v & 4 ? 4 : 2));
+          } else {
+            CHECK(p.pack.n == x_copied + w_copied && !p.b_wide);
+            CHECK((p.gemm.a.p == l.x) == !x_copied && (p.gemm.b.p == l.w) == !w_copied);
+          }
           // copies lie in the workspace, apart from one another
           uintptr_t end = (uintptr_t)at(512);
           for (int i = 0; i < p.pack.n; ++i) {
@@ -126,18 +132,28 @@ static void check_layers() {
                 {520, 20000, 1000, LIN_TILE_128}, {2048, 20000, 1032, LIN_TILE_256}};
   for (const auto& s : splits) CHECK(run(layer(s.m, s.k, s.n), false, &p) == MUON_OK && p.finish && p.tile == s.tile);
   CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && !p.finish);
-  // a matrix that is readable but for one thing
-  muon_linear_t l = layer(64, 64, 64);
-  CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 0 && p.workspace == 0);
-  l.x = at(64, 2);
-  CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 1);
-  l = layer(64, 64, 64);
-  l.ldx = 65;
-  CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 1);
-  l.ldx = 0;  // one row over and over
-  CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 1);
-  l.ldx = ((int64_t)1 << 22) + 8;
-  CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 1);
+  // a matrix that direct loads can read but for one thing: read through registers if it is
+  // small, through a copy if it is large or its rows are short
+  CHECK(run(layer(64, 64, 64), false, &p) == MUON_OK && p.pack.n == 0 && p.workspace == 0 && p.tile != LIN_TILE_64_ANY);
+  void (*const changes[])(muon_linear_t&) = {
+      [](muon_linear_t& l) { l.x = at(64, 2); },       [](muon_linear_t& l) { l.ldx += 1; },
+      [](muon_linear_t& l) { l.ldx = 0; },             [](muon_linear_t& l) { l.ldx = ((int64_t)1 << 22) + 8; },
+      [](muon_linear_t& l) { l.w_type = MUON_FP32; },  [](muon_linear_t& l) { l.ldw += 1; },
+  };
+  for (const auto& change : changes) {
+    muon_linear_t l = layer(64, 64, 64);
+    change(l);
+    CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 0 && p.workspace == 0 && p.tile == LIN_TILE_64_ANY);
+    CHECK(p.b_wide == (l.w_type == MUON_FP32));
+    l = layer(8192, 768, 3072);
+    change(l);
+    CHECK(run(l, false, &p) == MUON_OK && p.pack.n == 1 && p.workspace > 0 && p.tile != LIN_TILE_64_ANY && !p.b_wide);
+  }
+  for (int64_t k = 1; k <= 8; ++k) {
+    CHECK(run(layer(64, k, 64), false, &p) == MUON_OK && p.pack.n == (k < 8) && p.tile != LIN_TILE_64_ANY);
+    CHECK(run(layer(64, 64, k, true), true, &p) == MUON_OK && p.pack.n == (k < 8 ? 2 : 0) && p.tile != LIN_TILE_64_ANY);
+  }
+  muon_linear_t l;
   // no rows: nothing to do, whatever the pointers
   l = layer(0, 64, 64);
   l.x = l.y = nullptr;
@@ -190,8 +206,8 @@ static void check_refusals() {
       {"preact overlaps residual", [](muon_linear_t& l) { l.preact = at(300), l.ldp = 64, l.residual = at(300), l.ldr = 64; }},
       {"y overlaps residual", [](muon_linear_t& l) { l.residual = at(192, 2), l.ldr = 64; }},
       {"y overlaps rng", [](muon_linear_t& l) { l.rng = (const int64_t*)at(192, 8), l.dropout = 0.5f; }},
-      {"workspace overlaps x", [](muon_linear_t& l) { l.x = at(512, 2); }},
-      {"workspace overlaps w", [](muon_linear_t& l) { l.w = at(512), l.w_type = MUON_FP32; }},
+      {"workspace overlaps x", [](muon_linear_t& l) { l.k = 7, l.x = at(512, 2); }},
+      {"workspace overlaps w", [](muon_linear_t& l) { l.k = 7, l.w = at(512), l.w_type = MUON_FP32; }},
   };
   for (const Case& c : cases) {
     muon_linear_t l = layer(64, 64, 64);
@@ -242,9 +258,9 @@ static void check_refusals() {
   l.x = at(64, 136 * 2);
   CHECK(run(l) == MUON_OK);
   // the workspace
-  l = layer(64, 63, 64);
+  l = layer(64, 7, 64);
   size_t bytes = 0;
-  CHECK(linear_workspace(&l, false, &bytes) == MUON_OK && bytes >= 64 * 64 * 2);
+  CHECK(linear_workspace(&l, false, &bytes) == MUON_OK && bytes >= 64 * 8 * 2);
   CHECK(said(plan_linear(&l, false, nullptr, bytes, &p), MUON_EINVAL, "workspace is NULL"));
   CHECK(said(plan_linear(&l, false, at(512, 8), bytes, &p), MUON_EINVAL, "16-byte"));
   CHECK(said(plan_linear(&l, false, at(512), bytes - 1, &p), MUON_ENOMEM, "needs"));
@@ -312,7 +328,7 @@ static void check_grads() {
             }
           }
         }
-  CHECK(split && tiles.size() == 3 && !tiles.count(LIN_TILE_32) && !tiles.count(LIN_TILE_64_DEEP));
+  CHECK(split && tiles.size() == 4 && !tiles.count(LIN_TILE_32) && !tiles.count(LIN_TILE_64_DEEP));
   LinPlan p;
   CHECK(run(grad(72, 4097, 2311), &p) == MUON_OK && p.tile == LIN_TILE_256);
   CHECK(run(grad(200, 2000, 1100), &p) == MUON_OK && p.tile == LIN_TILE_128);

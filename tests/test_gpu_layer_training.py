@@ -196,8 +196,8 @@ def test_two_graphs_do_not_share_workspaces():
 def test_timing_families():
     import optimizer_muon_step_amd as mu
     rng = np.random.default_rng(61)
-    x, w, dz = make(rng, (64, 63), "bf16"), make(rng, (63, 72), "bf16"), make(rng, (64, 72), "bf16")
-    dw = make(rng, (63, 72), "fp32")
+    x, w, dz = make(rng, (64, 7), "bf16"), make(rng, (7, 72), "bf16"), make(rng, (64, 72), "bf16")
+    dw = make(rng, (7, 72), "fp32")  # x is copied first
     for kernel, call, launches in ((mu.KERNEL_LINEAR, lambda: mu.muon_linear(x, w), 2),
                                    (mu.KERNEL_LINEAR_DW, lambda: mu.muon_linear_dw(x, dz, dw), 2),
                                    (mu.KERNEL_DROPOUT, lambda: mu.muon_dropout(x, 0.5, (1, 2)), 1)):

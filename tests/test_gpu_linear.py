@@ -148,6 +148,46 @@ def test_split_epilogues(act, parts, out, kind, w_kind, shape):
     check_dx(mu, x, w.T, kind, out=out, act=act, preact=pre, residual=res, drop=drop)
 
 
+# read through a copy: rows shorter than 8, or products too large for 64 x 64 tiles
+COPIED = [(70, 5, 72), (300, 6, 7), (5000, 1001, 1003), (8200, 771, 1029)]
+
+
+@pytest.mark.parametrize("order", ["rows", "columns"])
+@pytest.mark.parametrize("w_kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", COPIED, ids=str)
+def test_copied_operands(shape, w_kind, order):
+    import optimizer_muon_step_amd as mu
+    m, k, n = shape
+    rng = np.random.default_rng(m + k * 3 + n)
+    say(f"[copied] {shape} {w_kind} {order}")
+    x, w = make(rng, (m, k), "bf16", offset=1, fill=NAN), make(rng, (k, n), w_kind, 0.1, order=order, fill=NAN)
+    check_linear(mu, x, w, "bf16")
+    dz = make(rng, (m, n), "bf16", 0.1, gap=3, fill=NAN)
+    check_dx(mu, dz, w, "bf16", residual=make(rng, (m, k), "bf16"))
+    check_dw(mu, x, dz, make(rng, (k, n), "fp32", order=order), "bf16", bias=True, add=True)
+
+
+# read through registers: rows of 8 elements up, that end inside a chunk of 8 or a tile, that lie apart
+# or anywhere, fp32 weights, a reduction of one slice to several splits
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("order", ["rows", "columns"])
+@pytest.mark.parametrize("m,k,n,gap,offset", [(1, 9, 8, 1, 1), (5, 8, 9, 0, 3), (64, 127, 65, 0, 0), (65, 128, 63, 1, 0),
+                                              (3, 129, 193, 2, 5), (1, 768, 768, 0, 1), (77, 257, 15, 0, 7), (33, 1031, 129, 5, 0),
+                                              (9, 10007, 71, 0, 2)])
+def test_any_rows(m, k, n, gap, offset, order, kind):
+    import optimizer_muon_step_amd as mu
+    rng = np.random.default_rng(m + k * 3 + n)
+    say(f"[any] {(m, k, n)} {gap} {offset} {order} {kind}")
+    x, dz = make(rng, (m, k), kind, 1.0, offset, gap, fill=NAN), make(rng, (m, n), kind, 0.1, offset, gap, fill=NAN)
+    for w_kind in (kind, "fp32"):
+        w = make(rng, (k, n), w_kind, 0.1, offset, gap, order=order, fill=NAN)
+        check_linear(mu, x, w, kind, act="gelu", bias=make(rng, (1, n), "fp32")[0], keep=True)
+        check_dx(mu, dz, w, kind, out="fp32")
+    dw = make(rng, (k, n), "fp32", offset=offset, gap=gap, order=order, fill=NAN)
+    check_dw(mu, x, dz, dw, kind, bias=True)
+    assert outside_unchanged(dw, NAN)
+
+
 def test_split_in_place_and_captured():
     """Two captured calls whose reductions are split, the output the residual, replayed among eager calls."""
     torch = torch_mod()

@@ -106,18 +106,25 @@ def test_far_rows_of_weights(order):
         assert torch.equal(dw, far_dw)
 
 
-def test_rows_too_far_for_the_kernels():
-    """More than 2^22 elements apart: read through a copy."""
+def test_rows_too_far_for_direct_loads():
+    """More than 2^22 elements apart: read through registers, or, of a large product, through a copy."""
     torch = torch_mod()
     import optimizer_muon_step_amd as mu
-    rng = np.random.default_rng(4)
     ld = (1 << 22) + 8
-    x, w, dz = make(rng, (70, 72), "bf16"), make(rng, (72, 88), "bf16"), make(rng, (70, 88), "bf16")
-    assert torch.equal(mu.muon_linear(x, w), mu.muon_linear(far(x, ld), far(w, ld)))
-    assert torch.equal(mu.muon_linear_dx(dz, w), mu.muon_linear_dx(far(dz, ld), far(w, ld)))
-    dw, far_dw = torch.empty(72, 88, device="cuda"), far(torch.empty(72, 88, device="cuda"), ld)
+    for m, k, n in ((70, 72, 88), (8192, 768, 3072)):
+        x, w, dz = signs((m, k), "bf16", 1), signs((k, n), "bf16", 2), signs((m, n), "bf16", 3)
+        far_w = far(w, ld)
+        say(f"[too far] {m} {k} {n}")
+        assert torch.equal(mu.muon_linear(x, w, out_dtype=torch.float32), mu.muon_linear(x, far_w, out_dtype=torch.float32))
+        assert torch.equal(mu.muon_linear_dx(dz, w, out_dtype=torch.float32), mu.muon_linear_dx(dz, far_w, out_dtype=torch.float32))
+        del far_w
+    m, k, n = 515, 72, 88
+    x, w, dz = signs((m, k), "fp16", 4), signs((k, n), "fp16", 5), signs((m, n), "fp16", 6)
+    far_x, far_dz = far(x, ld), far(dz, ld)
+    assert torch.equal(mu.muon_linear(x, w), mu.muon_linear(far_x, w))
+    dw, far_dw = torch.empty(k, n, device="cuda"), far(torch.empty(k, n, device="cuda"), ld)
     mu.muon_linear_dw(x, dz, dw)
-    mu.muon_linear_dw(far(x, ld), far(dz, ld), far_dw)
+    mu.muon_linear_dw(far_x, far_dz, far_dw)
     assert torch.equal(dw, far_dw)
 
 

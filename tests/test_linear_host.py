@@ -74,12 +74,12 @@ def test_entries_refuse_before_any_hip_call(lib):
     assert linear(lib.muon_linear, act=9) == -1 and "act" in text()
     assert linear(lib.muon_linear, dropout=1.5) == -1 and "dropout" in text()
     assert linear(lib.muon_linear, y=0x100000) == -1 and "overlaps" in text()
-    assert linear(lib.muon_linear, x=0x100002) == -1 and "workspace is NULL" in text()
-    assert linear(lib.muon_linear, x=0x100002, ws=0x500000, nbytes=64) == -2 and "needs" in text()
+    assert linear(lib.muon_linear, x=0x100002, k=7) == -1 and "workspace is NULL" in text()
+    assert linear(lib.muon_linear, x=0x100002, k=7, ws=0x500000, nbytes=64) == -2 and "needs" in text()
     assert linear(lib.muon_linear_dx, bias=0x400000, bias_type=1) == -1 and "bias" in text()
     assert linear(lib.muon_linear_dx, act=1) == -1 and "preact" in text()
     assert lib.muon_linear_workspace_bytes(ctypes.byref(_lib.MuonLinear(**good)), 0) == 0
-    assert lib.muon_linear_workspace_bytes(ctypes.byref(_lib.MuonLinear(**{**good, "w_type": 0})), 1) >= 64 * 64 * 2
+    assert lib.muon_linear_workspace_bytes(ctypes.byref(_lib.MuonLinear(**{**good, "w_type": 0, "n": 7})), 1) >= 2 * 64 * 8 * 2
     assert lib.muon_linear_workspace_bytes(ctypes.byref(_lib.MuonLinear(**{**good, "n": 0})), 0) == 0 and "n = 0" in text()
     dw = dict(m=64, k=64, n=64, x=0x100000, dz=0x200000, dw=0x300000, ldx=64, lddz=64, lddw=64, type=1)
     assert lib.muon_linear_dw(ctypes.byref(_lib.MuonLinearDw(**{**dw, "dw": 0x200000})), None, 0, None) == -1 and "overlaps" in text()
