@@ -22,6 +22,12 @@
 // global side, since each lane's LDS slot is fixed by its lane id.
 // WK > 1 gives the k-steps of a slice to WK groups of waves whose sums meet in LDS at the end: a
 // small tile then has enough waves.
+//
+// Measured (bf16, one MI355X): 16384 x 3072 over 768 with GELU and z kept 103 us, 750
+// TFLOP/s, 65 us of it the main loop and the rest 200 MB of stores that a round of tiles
+// ends with; 32768 x 6400 over 1600 685 us, 980 TFLOP/s, matrix cores busy 43 %: with 256 x 256 tiles
+// of 8 waves LDS reads and barriers take their turns beside them (at 8192^3 540 us of matrix instructions alone, 612
+// with the reads, 630 with barriers, 800 with the loads).  One row is latency, 5.8 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -37,7 +43,6 @@ namespace lin {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 #define LIN_LDS __attribute__((address_space(3)))
 
