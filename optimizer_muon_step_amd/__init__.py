@@ -55,6 +55,15 @@ def _current_device():
     return -1
 
 
+def _device_and_stream():
+    """The current GPU and the handle of torch's current stream on it; -1 and 0 where there is none."""
+    import torch
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        dev = torch.cuda.current_device()
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return -1, 0
+
+
 def _stream_handle(stream):
     if stream is None:
         import torch
@@ -430,10 +439,8 @@ def _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preac
     if stream is not None:
         with _on_stream(stream):
             return _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preact, backward, None)
-    dev = _current_device()
     rc, y = _lib.load_tensor_calls().linear(x, w, bias, _act_code(act), dropout, rng, site, residual, out,
-                                            _dtype_code(out_dtype), preact, backward, dev,
-                                            _stream_handle(None) if dev >= 0 else 0)
+                                            _dtype_code(out_dtype), preact, backward, *_device_and_stream())
     _check(rc)
     return y
 
@@ -447,8 +454,7 @@ def muon_linear_dw(x, dz, dw, dbias=None, accumulate=False, stream=None) -> None
     if stream is not None:
         with _on_stream(stream):
             return muon_linear_dw(x, dz, dw, dbias, accumulate)
-    dev = _current_device()
-    _check(_lib.load_tensor_calls().linear_dw(x, dz, dw, dbias, accumulate, dev, _stream_handle(None) if dev >= 0 else 0))
+    _check(_lib.load_tensor_calls().linear_dw(x, dz, dw, dbias, accumulate, *_device_and_stream()))
 
 
 def muon_dropout(x, p, rng, site=0, act=None, preact=None, residual=None, out=None, out_dtype=None, stream=None):
@@ -460,9 +466,8 @@ def muon_dropout(x, p, rng, site=0, act=None, preact=None, residual=None, out=No
     if stream is not None:
         with _on_stream(stream):
             return muon_dropout(x, p, rng, site, act, preact, residual, out, out_dtype)
-    dev = _current_device()
     rc, y = _lib.load_tensor_calls().dropout(x, p, rng, site, _act_code(act), preact, residual, out,
-                                             _dtype_code(out_dtype), dev, _stream_handle(None) if dev >= 0 else 0)
+                                             _dtype_code(out_dtype), *_device_and_stream())
     _check(rc)
     return y
 

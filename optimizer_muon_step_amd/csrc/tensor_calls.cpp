@@ -419,12 +419,24 @@ at::TensorOptions options(int code, int device) {
   return at::TensorOptions().dtype(scalar_type(code)).device(at::Device(at::kCUDA, (c10::DeviceIndex)device));
 }
 
-// Memory of the call's stream for what the library lays out on the way.
-at::Tensor workspace_of(size_t bytes, int device) {
-  if (bytes == 0) return {};
-  return at::empty({(int64_t)bytes}, options(MUON_FP32, device).dtype(at::kByte));
+// A call with memory of its stream as the workspace.  Most calls need none, and planning one
+// takes 0.3 us: it is made without first, and again if that was what it lacked.
+template <typename Call, typename Bytes>
+int with_workspace(int device, Call&& call, Bytes&& bytes_of) {
+  auto run = [&](void* p, size_t bytes) {
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(p, bytes);
+    Py_END_ALLOW_THREADS
+    return rc;
+  };
+  const int rc = run(nullptr, 0);
+  if (rc != MUON_EINVAL) return rc;
+  const size_t bytes = bytes_of();
+  if (bytes == 0) return run(nullptr, 0);  // refused for another reason: again, for its text
+  const at::Tensor ws = at::empty({(int64_t)bytes}, options(MUON_FP32, device).dtype(at::kByte));
+  return run(ws.data_ptr(), bytes);
 }
-void* ptr_or_null(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // (tensor given or new, code of the call) as Python has it.
 PyObject* finish_out(PyObject* given, const at::Tensor& fresh, int rc) {
@@ -524,12 +536,12 @@ PyObject* linear(PyObject*, PyObject* args) {
     l.step = rng.step;
     l.site = rng.site;
     l.rng = rng.device_state;
-    const size_t bytes = muon_linear_workspace_bytes(&l, backward);
-    const at::Tensor ws = workspace_of(bytes, device);
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = (backward ? muon_linear_dx : muon_linear)(&l, ptr_or_null(ws), bytes, (hipStream_t)(uintptr_t)stream);
-    Py_END_ALLOW_THREADS
+    const int rc = with_workspace(
+        device,
+        [&](void* ws, size_t bytes) {
+          return (backward ? muon_linear_dx : muon_linear)(&l, ws, bytes, (hipStream_t)(uintptr_t)stream);
+        },
+        [&] { return muon_linear_workspace_bytes(&l, backward); });
     if (rc == MUON_OK && pre && !backward) mark_written(*pre->t);
     return finish_out(out_o, fresh, rc);
   });
@@ -572,12 +584,9 @@ PyObject* linear_dw(PyObject*, PyObject* args) {
     l.type = x.type;
     l.dw_transposed = dw.transposed;
     l.accumulate = accumulate;
-    const size_t bytes = muon_linear_dw_workspace_bytes(&l);
-    const at::Tensor ws = workspace_of(bytes, device);
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = muon_linear_dw(&l, ptr_or_null(ws), bytes, (hipStream_t)(uintptr_t)stream);
-    Py_END_ALLOW_THREADS
+    const int rc = with_workspace(
+        device, [&](void* ws, size_t bytes) { return muon_linear_dw(&l, ws, bytes, (hipStream_t)(uintptr_t)stream); },
+        [&] { return muon_linear_dw_workspace_bytes(&l); });
     if (rc == MUON_OK) {
       mark_written(*dw.t);
       if (db) mark_written(*db);
