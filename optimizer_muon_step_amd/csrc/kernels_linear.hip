@@ -17,6 +17,7 @@ static hipError_t launch_tile(const LinGemmArgs& a, int tile, bool b_wide, hipSt
     case LIN_TILE_64: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 2, 2, 2, 2><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64_DEEP: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 1, 4, 4, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_32: linear_gemm_kernel<TYPE, false, BKM, false, 32, 64, 128, 1, 1, 4, 3, 2><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_32_DEEP: linear_gemm_kernel<TYPE, false, BKM, false, 32, 64, 128, 1, 1, 4, 6, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64_ANY:
       if (b_wide) linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 2, 2, 2, 2, READ_ANY_WIDE><<<grid, threads, 0, s>>>(a);
       else linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 2, 2, 2, 2, READ_ANY><<<grid, threads, 0, s>>>(a);

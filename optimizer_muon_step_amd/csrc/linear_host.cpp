@@ -130,7 +130,7 @@ struct TileCost {
   double one, one_slice, two, two_slice;  // two = 0: no second tile fits
 };
 constexpr TileCost kTileCost[LIN_TILES] = {
-    {9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24},
+    {9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24}, {3.1, 0.185, 0, 0},
     {4.0, 0.27, 5.0, 0.46}};
 constexpr double GRAD_SLICE = 1.17, UNALIGNED_SLICE = 1.45;
 
@@ -144,8 +144,8 @@ double tiles_us(int tile, int64_t tiles, double slices) {
 
 // A split leaves its sums in memory and a last pass adds them up: 3 us for the
 // launch, and the sums written and read at 5 TB/s.  For a layer of few rows (us, with and
-// without splits): 1 x 768 over 3072 7.3 and 12.7, 64 x 1600 over 6400 11.8 and
-// 20.9, 2048 x 1600 over 6400 57 and 70; 1 x 2304 over 768 is not split, 5.9.
+// without splits): 1 x 768 over 3072 6.8 and 12.0, 64 x 1600 over 6400 11.8 and
+// 20.9, 2048 x 1600 over 6400 57 and 70; 1 x 2304 over 768 is not split, 5.4.
 double splits_us(int64_t m, int64_t n, int64_t splits) { return splits == 1 ? 0 : 3.0 + (double)(m * n * splits) * 8 / 5e6; }
 
 // The copies that operands need in all tiles but 64_ANY: 3 us for the launch, their
@@ -183,10 +183,10 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies
   double best = 0;
   for (int tile = 0; tile < LIN_TILES; ++tile) {
     // few rows of a weight, or few weights over few rows, are no case worth a kernel
-    if (grad && (tile == LIN_TILE_32 || tile == LIN_TILE_64_DEEP)) continue;
+    if (grad && (tile == LIN_TILE_32 || tile == LIN_TILE_64_DEEP || tile == LIN_TILE_32_DEEP)) continue;
     if (tile == LIN_TILE_64_ANY && !copies.avoidable) continue;
-    // up to 32 rows it makes no more tiles, and each loads with fewer waves: one row of
-    // 2304 over 768 7.5 us, 5.5 in 64 x 64
+    // up to 32 rows the whole LDS serves one tile better: one row of 2304 over 768
+    // takes 7.5 us in it, 5.4 with the deep ring, 5.9 in 64 x 64 with its own
     if (tile == LIN_TILE_32 && m <= 32) continue;
     const bool any = tile == LIN_TILE_64_ANY;
     const double slower = (grad ? GRAD_SLICE : 1.0) * (any && copies.unaligned ? UNALIGNED_SLICE : 1.0);

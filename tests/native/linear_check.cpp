@@ -117,7 +117,7 @@ static void check_layers() {
   CHECK(tiles.size() == LIN_TILES);
   // the sizes by which the tests on the GPU mean to reach each tile
   LinPlan p;
-  CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_64_DEEP);
+  CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_32_DEEP);
   CHECK(run(layer(130, 200, 1000), false, &p) == MUON_OK && p.tile == LIN_TILE_32);
   CHECK(run(layer(1500, 72, 1304), false, &p) == MUON_OK && p.tile == LIN_TILE_64);
   CHECK(run(layer(1000, 2304, 760), false, &p) == MUON_OK && p.tile == LIN_TILE_64_DEEP);
@@ -128,7 +128,7 @@ static void check_layers() {
   const struct {
     int64_t m, k, n;
     int tile;
-  } splits[] = {{1, 4096, 72, LIN_TILE_64}, {64, 6400, 1600, LIN_TILE_64_DEEP}, {130, 9000, 200, LIN_TILE_32},
+  } splits[] = {{1, 4096, 72, LIN_TILE_32_DEEP}, {257, 30000, 520, LIN_TILE_64}, {64, 6400, 1600, LIN_TILE_64_DEEP}, {130, 9000, 200, LIN_TILE_32},
                 {520, 20000, 1000, LIN_TILE_128}, {2048, 20000, 1032, LIN_TILE_256}};
   for (const auto& s : splits) CHECK(run(layer(s.m, s.k, s.n), false, &p) == MUON_OK && p.finish && p.tile == s.tile);
   CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && !p.finish);

@@ -113,8 +113,8 @@ def test_linear_epilogues(act, parts, out, kind, w_kind, shape):
                  "keep" in parts)
 
 
-# few tiles and a long reduction, which is split: 64 x 64 tiles with either ring, 32 x 64, 128 x 128 and 256 x 256
-SPLIT = [(1, 4096, 72), (64, 6400, 1600), (9, 20001, 31), (257, 30000, 513), (130, 9000, 200), (520, 20000, 1000), (2048, 20000, 1032)]
+# few tiles and a long reduction, which is split, in tiles of each kind
+SPLIT = [(1, 4096, 72), (257, 30000, 520), (64, 6400, 1600), (9, 20001, 31), (257, 30000, 513), (130, 9000, 200), (520, 20000, 1000), (2048, 20000, 1032)]
 
 
 @pytest.mark.parametrize("order", ["rows", "columns"])
