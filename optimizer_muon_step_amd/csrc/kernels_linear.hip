@@ -13,6 +13,7 @@ static hipError_t launch_tile(const LinGemmArgs& a, int tile, bool b_wide, hipSt
   const int grid = a.tiles_m * a.tiles_n * a.splits, threads = kLinTile[tile].threads;
   switch (tile) {  // tile, K slice, waves along m, n and k, stages, blocks to a compute unit
     case LIN_TILE_256: linear_gemm_kernel<TYPE, false, BKM, false, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_256x192: linear_gemm_kernel<TYPE, false, BKM, false, 256, 192, 64, 4, 3, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_128: linear_gemm_kernel<TYPE, false, BKM, false, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 2, 2, 2, 2><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64_DEEP: linear_gemm_kernel<TYPE, false, BKM, false, 64, 64, 128, 2, 1, 4, 4, 1><<<grid, threads, 0, s>>>(a); break;

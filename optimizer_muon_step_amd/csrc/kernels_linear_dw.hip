@@ -14,6 +14,7 @@ static hipError_t launch_tile(const LinGemmArgs& a, int tile, hipStream_t s) {
   const int grid = a.tiles_m * a.tiles_n * a.splits, threads = kLinTile[tile].threads;
   switch (tile) {  // as in kernels_linear.hip
     case LIN_TILE_256: linear_gemm_kernel<TYPE, true, true, true, 256, 256, 64, 2, 4, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
+    case LIN_TILE_256x192: linear_gemm_kernel<TYPE, true, true, true, 256, 192, 64, 4, 3, 1, 2, 1><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_128: linear_gemm_kernel<TYPE, true, true, true, 128, 128, 64, 2, 2, 1, 2, 2><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 128, 2, 2, 2, 2, 2><<<grid, threads, 0, s>>>(a); break;
     case LIN_TILE_64_ANY: linear_gemm_kernel<TYPE, true, true, true, 64, 64, 128, 2, 2, 2, 2, 2, READ_ANY><<<grid, threads, 0, s>>>(a); break;

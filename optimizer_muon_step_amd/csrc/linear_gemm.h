@@ -95,12 +95,12 @@ __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
 template <bool KMAJOR, int R, int NW, int BK>
 struct Slice {
   static constexpr int BYTES = R * BK * 2;
-  static constexpr int LOADS = BYTES / 1024 / NW;   // 1 KB each, per wave
+  static constexpr int PIECES = BYTES / 1024, LOADS = (PIECES + NW - 1) / NW;  // 1 KB each, per wave
   static constexpr int PITCH = KMAJOR ? R * 2 : BK * 2;  // bytes of a row
   static constexpr int CHUNKS = PITCH / 16;  // 16-byte chunks of a row
-  static_assert(R % 32 == 0 && LOADS >= 1 && LOADS * 1024 * NW == BYTES, "tile does not split into whole loads");
+  static_assert(R % 32 == 0 && PIECES * 1024 == BYTES && PIECES >= NW, "tile does not split into whole loads");
   static_assert(BK == 128 || BK == 64, "k-contiguous rows of 256 or 128 bytes");
-  static_assert(!KMAJOR || R == 64 || R == 128 || R == 256, "k-major rows of 128, 256 or 512 bytes");
+  static_assert(!KMAJOR || R % 64 == 0, "k-major rows of multiples of 128 bytes: the swizzle stays within 8 chunks");
 
   // Chunk swizzle.  A k-contiguous fragment has 16 lanes on 16 rows at one
   // chunk; a row of 128 elements fills a 256-byte line of the banks and two rows of
@@ -108,6 +108,11 @@ struct Slice {
   // chunks.  A transposing read has each 16 lanes on 4 rows, 32 bytes each, and the
   // next 16 lanes 8 rows further on; the XOR sends the 4 rows to different 64-byte
   // groups of the banks and the 8 rows to the other half of such a group.
+  // Piece t of a wave.  Where they do not divide, some waves load the last one too: each
+  // has the same number of loads to wait for.
+  static __device__ __forceinline__ int piece(int t, int wave) {
+    return PIECES % NW == 0 ? t * NW + wave : min(t * NW + wave, PIECES - 1);
+  }
   static __device__ __forceinline__ int swz(int row, int chunk) {
     if (!KMAJOR) return BK == 64 ? chunk ^ ((row >> 1) & 7) : chunk ^ (row & 15);
     return chunk ^ (PITCH % 256 != 0 ? 4 * ((row >> 1) & 1) : 4 * (row & 3)) ^ (2 * ((row >> 3) & 1));
@@ -126,7 +131,7 @@ struct Slice {
     left = o.bytes - at;
 #pragma unroll
     for (int t = 0; t < LOADS; ++t) {
-      const int slot = (t * NW + wave) * 64 + lane, row = slot / CHUNKS;
+      const int slot = piece(t, wave) * 64 + lane, row = slot / CHUNKS;
       vo[t] = (uint32_t)(row * (int)o.ld) + swz(row, slot % CHUNKS) * 16;
     }
   }
@@ -140,10 +145,10 @@ struct Slice {
     for (int t = 0; t < LOADS; ++t) {
       uint32_t off = vo[t];
       if (!KMAJOR && have < BK) {  // the chunk that K ends in holds zeros from there on
-        const int slot = (t * NW + wave) * 64 + lane;
+        const int slot = piece(t, wave) * 64 + lane;
         if (swz(slot / CHUNKS, slot % CHUNKS) * 8 >= have) off = 0x80000000u;
       }
-      load_to_lds(rsrc, (uint32_t)(uintptr_t)(to + (t * NW + wave) * 1024), off, t == 0);
+      load_to_lds(rsrc, (uint32_t)(uintptr_t)(to + piece(t, wave) * 1024), off, t == 0);
     }
     base += step;
     left -= step;
@@ -189,6 +194,7 @@ struct AnySlice : Slice<KMAJOR, R, NW, BK> {
   typedef Slice<KMAJOR, R, NW, BK> Base;
   using Base::CHUNKS;
   using Base::LOADS;
+  static_assert(Base::PIECES % NW == 0, "whole loads");
   using Base::swz;
   static constexpr int SIZE = WIDE ? 4 : 2;
   struct Held {

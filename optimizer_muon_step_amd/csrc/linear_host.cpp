@@ -122,15 +122,15 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // Microseconds of a round of tiles over the 256 compute units, as measured (bf16, one MI355X):
 // a start and an end and so much for each 64 of K; one tile to a unit, or the two
 // that small tiles leave room for.  Over a K of 768 a round of 256 x 256 tiles
-// takes 26.6, of 128 x 128 13.2 and 19, of 64 x 64 6.2 and 8.8, of 32 x 64 5.3 and
-// 6.9; over 3072 77, 35 and 49, 14 and 22, 12 and 16.  Two k-major operands (a weight
-// gradient's) take 1.17 of that a slice, and rows that do not start at
+// takes 26.6, of 256 x 192 21.8, of 128 x 128 13.2 and 19, of 64 x 64 6.2 and 8.8, of 32 x 64 5.3 and
+// 6.9; over 3072 77, 64, 35 and 49, 14 and 22, 12 and 16.  Two k-major operands (a weight
+// gradient's) take 1.17 of that a slice, except in 256 x 192 tiles, and rows that do not start at
 // multiples of 16 bytes, loaded through registers, 1.45.
 struct TileCost {
   double one, one_slice, two, two_slice;  // two = 0: no second tile fits
 };
 constexpr TileCost kTileCost[LIN_TILES] = {
-    {9.7, 1.41, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24}, {3.1, 0.185, 0, 0},
+    {9.7, 1.41, 0, 0}, {7.6, 1.18, 0, 0}, {6.0, 0.6, 9.0, 0.83}, {3.6, 0.23, 4.5, 0.36}, {3.7, 0.205, 0, 0}, {3.1, 0.185, 4.0, 0.24}, {3.1, 0.185, 0, 0},
     {4.0, 0.27, 5.0, 0.46}};
 constexpr double GRAD_SLICE = 1.17, UNALIGNED_SLICE = 1.45;
 
@@ -167,8 +167,9 @@ struct Copies {
 };
 
 // Tiles, slices and splits of a product: what the measured times make the
-// fastest.  Examples (us, chosen and next): 16384 x 3072 over 768 82 in 256 x 256
-// tiles, 90 in 128 x 128; 8192 x 2304 over 768 43 in 128 x 128, 55 in 256 x 256;
+// fastest.  Examples (us, chosen and next): 16384 x 3072 over 768 90 in 256 x 256
+// tiles, 101 in 256 x 192; 16384 x 768 over 3072 67 in 256 x 192 (256 tiles, one to a unit), 79 in
+// 256 x 256; 4096 x 768 over 768 12.2 in 128 x 128, 19.1 in 256 x 192;
 // 1024 x 768 over 2304 11.4 in 64 x 64 with the deep ring, 12.6 with the other, 28
 // in 128 x 128; 512 x 768 over 3072 12.2 in 32 x 64, 13.4 in 64 x 64.
 //
@@ -189,7 +190,7 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies
     // takes 7.5 us in it, 5.4 with the deep ring, 5.9 in 64 x 64 with its own
     if (tile == LIN_TILE_32 && m <= 32) continue;
     const bool any = tile == LIN_TILE_64_ANY;
-    const double slower = (grad ? GRAD_SLICE : 1.0) * (any && copies.unaligned ? UNALIGNED_SLICE : 1.0);
+    const double slower = (grad && tile != LIN_TILE_256x192 ? GRAD_SLICE : 1.0) * (any && copies.unaligned ? UNALIGNED_SLICE : 1.0);
     const LinTileSize t = kLinTile[tile];
     const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn, tiles = tm * tn;
     const int slices = ceil_div(k, t.bk);

@@ -117,12 +117,12 @@ static_assert(sizeof(LinJoinArgs) <= KERNARG_BYTES, "kernel arguments");
 
 // Output tiles of the product kernels (see kernels_linear.hip and linear_host.cpp).
 // 64_DEEP and 32_DEEP have the whole LDS of a compute unit for their ring; 64_ANY loads through registers.
-enum LinTile { LIN_TILE_256 = 0, LIN_TILE_128, LIN_TILE_64, LIN_TILE_64_DEEP, LIN_TILE_32, LIN_TILE_32_DEEP, LIN_TILE_64_ANY, LIN_TILES };
+enum LinTile { LIN_TILE_256 = 0, LIN_TILE_256x192, LIN_TILE_128, LIN_TILE_64, LIN_TILE_64_DEEP, LIN_TILE_32, LIN_TILE_32_DEEP, LIN_TILE_64_ANY, LIN_TILES };
 struct LinTileSize {
   int bm, bn, bk, threads;
 };
 constexpr LinTileSize kLinTile[LIN_TILES] = {
-    {256, 256, 64, 512}, {128, 128, 64, 256}, {64, 64, 128, 512}, {64, 64, 128, 512}, {32, 64, 128, 256}, {32, 64, 128, 256}, {64, 64, 128, 512}};
+    {256, 256, 64, 512}, {256, 192, 64, 768}, {128, 128, 64, 256}, {64, 64, 128, 512}, {64, 64, 128, 512}, {32, 64, 128, 256}, {32, 64, 128, 256}, {64, 64, 128, 512}};
 
 // Dropout by itself.
 struct DropArgs {

@@ -122,14 +122,15 @@ static void check_layers() {
   CHECK(run(layer(1500, 72, 1304), false, &p) == MUON_OK && p.tile == LIN_TILE_64);
   CHECK(run(layer(1000, 2304, 760), false, &p) == MUON_OK && p.tile == LIN_TILE_64_DEEP);
   CHECK(run(layer(2000, 200, 1100), false, &p) == MUON_OK && p.tile == LIN_TILE_128);
-  CHECK(run(layer(4097, 72, 2311), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
-  CHECK(run(layer(4160, 136, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
+  CHECK(run(layer(4097, 72, 2311), false, &p) == MUON_OK && p.tile == LIN_TILE_256x192);
+  CHECK(run(layer(4160, 136, 2304), false, &p) == MUON_OK && p.tile == LIN_TILE_256x192);
+  CHECK(run(layer(8200, 72, 1400), false, &p) == MUON_OK && p.tile == LIN_TILE_256);
   // and with its reduction split
   const struct {
     int64_t m, k, n;
     int tile;
   } splits[] = {{1, 4096, 72, LIN_TILE_32_DEEP}, {257, 30000, 520, LIN_TILE_64}, {64, 6400, 1600, LIN_TILE_64_DEEP}, {130, 9000, 200, LIN_TILE_32},
-                {520, 20000, 1000, LIN_TILE_128}, {2048, 20000, 1032, LIN_TILE_256}};
+                {520, 20000, 1000, LIN_TILE_128}, {2048, 20000, 1032, LIN_TILE_256x192}, {1500, 20000, 1500, LIN_TILE_256}};
   for (const auto& s : splits) CHECK(run(layer(s.m, s.k, s.n), false, &p) == MUON_OK && p.finish && p.tile == s.tile);
   CHECK(run(layer(1, 768, 2304), false, &p) == MUON_OK && !p.finish);
   // a matrix that direct loads can read but for one thing: read through registers if it is
@@ -328,9 +329,10 @@ static void check_grads() {
             }
           }
         }
-  CHECK(split && tiles.size() == 4 && !tiles.count(LIN_TILE_32) && !tiles.count(LIN_TILE_64_DEEP));
+  CHECK(split && tiles.size() == 5 && !tiles.count(LIN_TILE_32) && !tiles.count(LIN_TILE_64_DEEP));
   LinPlan p;
-  CHECK(run(grad(72, 4097, 2311), &p) == MUON_OK && p.tile == LIN_TILE_256);
+  CHECK(run(grad(72, 4097, 2311), &p) == MUON_OK && p.tile == LIN_TILE_256x192);
+  CHECK(run(grad(72, 8200, 1400), &p) == MUON_OK && p.tile == LIN_TILE_256);
   CHECK(run(grad(200, 2000, 1100), &p) == MUON_OK && p.tile == LIN_TILE_128);
   CHECK(run(grad(4100, 72, 200), &p) == MUON_OK && p.finish);
   CHECK(run(grad(30000, 520, 264), &p) == MUON_OK && p.finish);

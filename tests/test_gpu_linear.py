@@ -75,7 +75,7 @@ def test_linear_shapes(shape, order, kind):
     check_linear(mu, x, w, kind, out="fp32", bias=b, act="gelu", keep=True, what="gelu")
 
 
-LARGE = [(4097, 72, 2311), (4160, 136, 2304), (1500, 72, 1304), (2000, 200, 1100), (3000, 72, 264), (1000, 2304, 760)]
+LARGE = [(8200, 72, 1400), (4097, 72, 2311), (4160, 136, 2304), (1500, 72, 1304), (2000, 200, 1100), (3000, 72, 264), (1000, 2304, 760)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
@@ -114,7 +114,7 @@ def test_linear_epilogues(act, parts, out, kind, w_kind, shape):
 
 
 # few tiles and a long reduction, which is split, in tiles of each kind
-SPLIT = [(1, 4096, 72), (257, 30000, 520), (64, 6400, 1600), (9, 20001, 31), (257, 30000, 513), (130, 9000, 200), (520, 20000, 1000), (2048, 20000, 1032)]
+SPLIT = [(1, 4096, 72), (257, 30000, 520), (64, 6400, 1600), (9, 20001, 31), (257, 30000, 513), (130, 9000, 200), (520, 20000, 1000), (2048, 20000, 1032), (1500, 20000, 1500)]
 
 
 @pytest.mark.parametrize("order", ["rows", "columns"])
