@@ -73,13 +73,10 @@ __device__ __forceinline__ void block_barrier() {
 // before every LDS read the compiler would wait for all of its own such loads,
 // those of later slices among them; the waits are wait_loads'.  It has no
 // result in registers, and nothing else in these kernels uses M0.  M0 has to be
-// set one wait state ahead, and a descriptor that a vector instruction left
-// (`fresh`) five.
-__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t to, uint32_t off, bool fresh) {
-  if (fresh)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(rsrc) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(rsrc) : "memory");
+// set one wait state ahead, and a descriptor that a vector instruction left (a
+// spilled scalar's way back, too) five.
+__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t to, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(rsrc) : "memory");
 }
 
 template <int TYPE>
@@ -148,7 +145,7 @@ struct Slice {
         const int slot = piece(t, wave) * 64 + lane;
         if (swz(slot / CHUNKS, slot % CHUNKS) * 8 >= have) off = 0x80000000u;
       }
-      load_to_lds(rsrc, (uint32_t)(uintptr_t)(to + piece(t, wave) * 1024), off, t == 0);
+      load_to_lds(rsrc, (uint32_t)(uintptr_t)(to + piece(t, wave) * 1024), off);
     }
     base += step;
     left -= step;
