@@ -105,12 +105,13 @@ hipError_t launch_dropout(const DropArgs& a, int64_t blocks, hipStream_t s) {
 }
 
 // Operands copied to rows that are aligned and a multiple of 8 long, with
-// zeros behind their ends; an eight to a thread.  1999 x 1001 fp16 and 1001 x 771 fp32, 12 MB
-// in all, 6.4 us.
-__global__ __launch_bounds__(PACK_THREADS) void linear_pack_kernel(const LinPackArgs a, int blocks0) {
-  const bool second = (int)blockIdx.x >= blocks0;
+// zeros behind their ends; an eight to a thread, in several launches where a grid cannot hold
+// the blocks.  1999 x 1001 fp16 and 1001 x 771 fp32, 12 MB in all, 6.4 us.
+__global__ __launch_bounds__(PACK_THREADS) void linear_pack_kernel(const LinPackArgs a, int64_t blocks0, int64_t first) {
+  const int64_t block = first + blockIdx.x;
+  const bool second = block >= blocks0;
   const LinPack& p = a.job[second];
-  const Eight at((int64_t)((int)blockIdx.x - (second ? blocks0 : 0)) * PACK_THREADS, threadIdx.x, p.rows, p.cols);
+  const Eight at((block - (second ? blocks0 : 0)) * PACK_THREADS, threadIdx.x, p.rows, p.cols);
   if (at.have == 0) return;
   const int64_t src = at.row * p.src_ld + at.col, dst = at.row * p.dst_ld + at.col;
   if (p.src_type != GRAD_FP32)  // either 16-bit type: the widened bits go back as they were
@@ -123,8 +124,10 @@ __global__ __launch_bounds__(PACK_THREADS) void linear_pack_kernel(const LinPack
 
 hipError_t launch_linear_pack(const LinPackArgs& a, hipStream_t s) {
   const int64_t b0 = pack_blocks(a.job[0]), b1 = a.n > 1 ? pack_blocks(a.job[1]) : 0;
-  linear_pack_kernel<<<(int)(b0 + b1), PACK_THREADS, 0, s>>>(a, (int)b0);
-  return hipGetLastError();
+  return (hipError_t)for_launches(b0 + b1, [&](int64_t first, int blocks) {
+    linear_pack_kernel<<<blocks, PACK_THREADS, 0, s>>>(a, b0, first);
+    return (int)hipGetLastError();
+  });
 }
 
 }  // namespace muon

@@ -378,9 +378,6 @@ int plan_grad(const muon_linear_dw_t* l, void* workspace, bool sizes_only, LinPl
 // The workspace as the caller gave it.
 int check_workspace(const LinPlan& p, const void* workspace, size_t bytes) {
   if (p.empty || p.workspace == 0) return MUON_OK;
-  int64_t copied = 0;  // blocks of the copies
-  for (int i = 0; i < p.pack.n; ++i) copied += pack_blocks(p.pack.job[i]);
-  if (copied > MAX_LAUNCH_ITEMS) return fail(MUON_EINVAL, "operands that have to be copied are too large");
   if (!workspace) return fail(MUON_EINVAL, "workspace is NULL; this call needs %zu bytes", p.workspace);
   if ((uintptr_t)workspace % 16) return fail(MUON_EINVAL, "workspace is not 16-byte aligned");
   if (bytes < p.workspace) return fail(MUON_ENOMEM, "workspace of %zu bytes; this call needs %zu", bytes, p.workspace);

@@ -64,6 +64,17 @@ constexpr int64_t pack_blocks(const LinPack& p) {
   return (p.rows * ((p.cols + 7) / 8) + PACK_THREADS - 1) / PACK_THREADS;
 }
 
+// `blocks` in launches of at most MAX_LAUNCH_ITEMS: f(first block, blocks), which gives 0, or
+// what ends the sequence and is given back.
+template <typename F>
+int for_launches(int64_t blocks, F&& f) {
+  for (int64_t first = 0; first < blocks; first += MAX_LAUNCH_ITEMS) {
+    const int64_t left = blocks - first;
+    if (const int rc = f(first, (int)(left < MAX_LAUNCH_ITEMS ? left : MAX_LAUNCH_ITEMS))) return rc;
+  }
+  return 0;
+}
+
 // One product C = A B, m x n over k.  Output tiles are numbered in groups of
 // LIN_GROUP tile rows, column by column within a group, and each XCD takes a run
 // of them: the 32 tiles that its compute units hold at a time then share 8

@@ -1,0 +1,106 @@
+// Host check of what the layer products take at the limits of a launch
+// (csrc/linear_host.cpp, linear_types.h): copies of more blocks than a launch
+// has go out in several.  Built and run by tests/test_linear_limits.py, under
+// sanitizers.  Prints "ok" and exits 0 when every check holds.
+#include <cstdio>
+#include <string>
+#include <vector>
+
+#include "linear_host.h"
+#include "plan_host.h"
+
+using namespace muon;
+
+static int g_failures = 0;
+#define CHECK(cond)                                                                   \
+  do {                                                                                \
+    if (!(cond)) {                                                                    \
+      std::fprintf(stderr, "%s:%d: check failed: %s\n", __FILE__, __LINE__, #cond); \
+      ++g_failures;                                                                   \
+    }                                                                                 \
+  } while (0)
+
+// Addresses are only compared, never followed.
+static void* at(uint64_t tib) { return (void*)(uintptr_t)(tib << 40); }
+
+static muon_linear_t layer(int64_t m, int64_t k, int64_t n) {
+  muon_linear_t l = {};
+  l.m = m;
+  l.k = k;
+  l.n = n;
+  l.x = at(1);
+  l.w = at(2);
+  l.y = at(3);
+  l.ldx = k;
+  l.ldw = l.ldy = n;
+  l.x_type = l.w_type = l.y_type = MUON_BF16;
+  return l;
+}
+
+static muon_linear_dw_t grad(int64_t m, int64_t k, int64_t n) {
+  muon_linear_dw_t l = {};
+  l.m = m;
+  l.k = k;
+  l.n = n;
+  l.x = at(1);
+  l.dz = at(2);
+  l.dw = (float*)at(3);
+  l.ldx = k;
+  l.lddz = l.lddw = n;
+  l.type = MUON_FP16;
+  return l;
+}
+
+static int run(const muon_linear_t& l, LinPlan* out) {
+  size_t bytes = 0;
+  linear_workspace(&l, false, &bytes);
+  const int rc = plan_linear(&l, false, at(16), bytes, out);
+  if (rc) std::fprintf(stderr, "  %lld x %lld x %lld: %s\n", (long long)l.m, (long long)l.k, (long long)l.n, last_error_text());
+  return rc;
+}
+
+static int run(const muon_linear_dw_t& l, LinPlan* out) {
+  size_t bytes = 0;
+  linear_dw_workspace(&l, &bytes);
+  const int rc = plan_linear_dw(&l, at(16), bytes, out);
+  if (rc) std::fprintf(stderr, "  dw %lld x %lld x %lld: %s\n", (long long)l.m, (long long)l.k, (long long)l.n, last_error_text());
+  return rc;
+}
+
+static int64_t copied_blocks(const LinPlan& p) {
+  int64_t blocks = 0;
+  for (int i = 0; i < p.pack.n; ++i) blocks += pack_blocks(p.pack.job[i]);
+  return blocks;
+}
+
+// Copies below, at and above the blocks of one launch.
+static void check_copies() {
+  LinPlan p;
+  // 256 rows of 128 are 16 blocks: the last whole launch ends at 2^28 - 16 rows
+  for (int64_t m : {((int64_t)1 << 28) - 16, (int64_t)1 << 28, ((int64_t)1 << 28) + 1}) {
+    CHECK(run(layer(m, 127, 192), &p) == MUON_OK);
+    CHECK(run(grad(m, 127, 5), &p) == MUON_OK && p.pack.n == 2 && copied_blocks(p) > MAX_LAUNCH_ITEMS);
+    CHECK(p.workspace >= (size_t)m * (128 + 8) * 2);
+  }
+  for (int64_t blocks : {(int64_t)0, (int64_t)1, MAX_LAUNCH_ITEMS - 1, MAX_LAUNCH_ITEMS, MAX_LAUNCH_ITEMS + 1, 5 * MAX_LAUNCH_ITEMS,
+                         5 * MAX_LAUNCH_ITEMS + 7}) {
+    int64_t next = 0;
+    std::vector<int> launches;
+    const int rc = for_launches(blocks, [&](int64_t first, int n) {
+      CHECK(first == next && n > 0 && n <= MAX_LAUNCH_ITEMS);
+      next = first + n;
+      launches.push_back(n);
+      return 0;
+    });
+    CHECK(rc == 0 && next == blocks && (int64_t)launches.size() == (blocks + MAX_LAUNCH_ITEMS - 1) / MAX_LAUNCH_ITEMS);
+  }
+  int calls = 0;
+  CHECK(for_launches(3 * MAX_LAUNCH_ITEMS, [&](int64_t, int) { return ++calls == 2 ? 7 : 0; }) == 7 && calls == 2);
+}
+
+int main() {
+  check_copies();
+  if (g_failures) return 1;
+  std::puts("ok");
+  return 0;
+}
