@@ -334,7 +334,8 @@ int muon_step_clip(float* const* params, const float* const* grads, float* const
  * Fields of muon_linear_t (for muon_linear_dx x is dz, m x n, y is dx, m x k,
  * residual is m x k and preact, read, m x k):
  *   m, k, n   m 0 .. MUON_LINEAR_MAX_ROWS; k, n 1 .. MUON_LINEAR_MAX_WIDTH;
- *             m = 0 does nothing
+ *             m = 0 does nothing.  Outputs of 2^23 tiles of 256 x 256
+ *             and more (over 500 GB) are refused
  *   x, w, residual, y, preact  device; elements of a row adjacent, rows ldx, ldw,
  *             ldr, ldy, ldp elements apart, any alignment of the element
  *             type.  w_transposed = 1: w is stored n x k (ldw from row to row of k).

@@ -198,6 +198,7 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies
       const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, slices * t.bk / 256);
       if (fill > 0 && want < 2) continue;
       const int per = slices ? ceil_div(slices, want) : 0, splits = slices ? ceil_div(slices, per) : 1;
+      if (tiles * splits >= ((int64_t)1 << 32) / t.threads) continue;  // a grid holds fewer than 2^32 threads
       const double us = tiles_us(tile, tiles * splits, per * t.bk / 64.0 * slower) + splits_us(m, n, splits) + (any ? 0 : copies.us);
       if (best != 0 && us >= best) continue;
       best = us;
@@ -205,12 +206,11 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies
       g.slices = slices;
       g.per_split = per;
       g.splits = splits;
-      g.tiles_m = (int32_t)std::min<int64_t>(tm, INT32_MAX);
+      g.tiles_m = (int32_t)tm;
       g.tiles_n = (int32_t)tn;
     }
   }
-  // a grid holds fewer than 2^32 threads
-  if ((int64_t)g.tiles_m * g.tiles_n * g.splits >= ((int64_t)1 << 32) / kLinTile[p->tile].threads)
+  if (best == 0)  // 2^23 tiles of 256 x 256 or more: no device has memory for so large an output
     return fail(MUON_EINVAL, "a product of %lld x %lld is too large", (long long)m, (long long)n);
   return MUON_OK;
 }

@@ -1,6 +1,6 @@
 // Host check of what the layer products take at the limits of a launch
-// (csrc/linear_host.cpp, linear_types.h): copies of more blocks than a launch
-// has go out in several.  Built and run by tests/test_linear_limits.py, under
+// (csrc/linear_host.cpp, linear_types.h): tiles that a grid cannot hold are passed
+// over for others, and copies of more blocks than a launch has go out in several.  Built and run by tests/test_linear_limits.py, under
 // sanitizers.  Prints "ok" and exits 0 when every check holds.
 #include <cstdio>
 #include <string>
@@ -98,7 +98,47 @@ static void check_copies() {
   CHECK(for_launches(3 * MAX_LAUNCH_ITEMS, [&](int64_t, int) { return ++calls == 2 ? 7 : 0; }) == 7 && calls == 2);
 }
 
+// A grid holds fewer than 2^32 threads.
+static void check_grid(const LinPlan& p, int64_t m, int64_t n) {
+  const LinTileSize t = kLinTile[p.tile];
+  CHECK((int64_t)p.gemm.tiles_m * p.gemm.tiles_n * p.gemm.splits * t.threads < (int64_t)1 << 32);
+  CHECK((int64_t)p.gemm.tiles_m * t.bm >= m && (int64_t)p.gemm.tiles_n * t.bn >= n);
+}
+
+static void check_grids() {
+  LinPlan p;
+  const int64_t most = (int64_t)1 << 30;
+  // the most rows, short enough to be read where they lie
+  CHECK(run(layer(most, 8, 8), &p) == MUON_OK && p.pack.n == 0 && p.workspace == 0 && p.tile == LIN_TILE_256x192);
+  check_grid(p, most, 8);
+  // the last row count whose 64 x 64 tiles of 512 threads a grid holds, and the first beyond it
+  const int64_t last = (((int64_t)1 << 23) - 1) * 64;
+  CHECK(run(layer(last, 61, 8), &p) == MUON_OK && p.tile == LIN_TILE_64_ANY && p.pack.n == 0);
+  check_grid(p, last, 8);
+  CHECK(run(layer(last + 1, 61, 8), &p) == MUON_OK && p.tile != LIN_TILE_64_ANY && p.pack.n == 1);
+  check_grid(p, last + 1, 8);
+  for (int64_t m : {((int64_t)1 << 28) + 1, ((int64_t)1 << 29) - 1, (int64_t)1 << 29, most - 1, most})
+    for (int64_t k : {1, 8, 25, 57, 61, 64, 127})
+      for (int64_t n : {1, 8, 61, 64, 192, 256}) {
+        CHECK(run(layer(m, k, n), &p) == MUON_OK);
+        check_grid(p, m, n);
+      }
+  for (int64_t k : {(int64_t)1 << 20, (int64_t)1 << 22})
+    for (int64_t n : {100, 1000, 100000}) {
+      CHECK(run(grad(100, k, n), &p) == MUON_OK);
+      check_grid(p, k, n);
+    }
+  // 2^23 tiles of 256 x 256, more than any device's memory: refused
+  CHECK(run(layer(most - 255, 64, 256), &p) == MUON_OK);
+  CHECK(run(layer(most, 64, 257), &p) == MUON_EINVAL && std::string(last_error_text()).find("too large") != std::string::npos);
+  CHECK(run(grad(64, (int64_t)1 << 22, (int64_t)1 << 22), &p) == MUON_EINVAL);
+  size_t bytes = 1;
+  const muon_linear_t l = layer(most, 64, 257);
+  CHECK(linear_workspace(&l, false, &bytes) == MUON_EINVAL && bytes == 0);
+}
+
 int main() {
+  check_grids();
   check_copies();
   if (g_failures) return 1;
   std::puts("ok");

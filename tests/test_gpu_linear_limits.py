@@ -48,3 +48,16 @@ def test_copies_of_more_blocks_than_a_launch():
         want += (x[a:a + step].float().T @ grad).double()
         want_db += grad.double().sum(0)
     assert torch.equal(dw.double(), want) and torch.equal(db.double(), want_db)
+
+
+def test_more_tiles_than_a_launch():
+    """2^29 + 3 rows of 61 into 8: 64 x 64 tiles, the fastest for such rows, would be 2^32 threads."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    m, k, n, step = (1 << 29) + 3, 61, 8, 1 << 24
+    x, w = sliding(m, k, "fp16", 4), signs((k, n), "fp16", 5)
+    say("[forward]")
+    y = mu.muon_linear(x, w)
+    assert y.shape == (m, n)
+    for a in range(0, m, step):
+        assert torch.equal(y[a:a + step].float(), x[a:a + step].float() @ w.float()), a
