@@ -60,7 +60,9 @@ def _device_and_stream():
     import torch
     if torch.cuda.is_initialized() or torch.cuda.is_available():
         dev = torch.cuda.current_device()
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+        _refuse_per_thread(handle)  # a workspace would belong to one stream and be used on several
+        return dev, handle
     return -1, 0
 
 

@@ -59,3 +59,21 @@ def test_refusals_do_not_depend_on_the_memory_left():
     with pytest.raises(mu.MuonError, match="y overlaps preact"):
         mu.muon_linear(x, w, out=y, preact=y)
     assert torch.cuda.max_memory_allocated() == before
+
+
+def test_the_per_thread_stream_is_refused():
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    x, w = torch.zeros(64, 67, dtype=torch.bfloat16, device="cuda"), torch.zeros(67, 131, dtype=torch.bfloat16, device="cuda")
+    y, dw = torch.zeros(64, 131, dtype=torch.bfloat16, device="cuda"), torch.zeros(67, 131, device="cuda")
+    per_thread = torch.cuda.ExternalStream(2)
+    calls = [lambda **s: mu.muon_linear(x, w, **s), lambda **s: mu.muon_linear_dx(y, w, **s),
+             lambda **s: mu.muon_linear_dw(x, y, dw, **s), lambda **s: mu.muon_dropout(x, 0.1, (1, 2), **s)]
+    for call in calls:
+        with pytest.raises(ValueError, match="hipStreamPerThread"):
+            call(stream=per_thread)
+        with torch.cuda.stream(per_thread), pytest.raises(ValueError, match="hipStreamPerThread"):
+            call()
+        call(stream=torch.cuda.Stream())
+        call(stream=0)
+    torch.cuda.synchronize()
