@@ -137,7 +137,46 @@ static void check_grids() {
   CHECK(linear_workspace(&l, false, &bytes) == MUON_EINVAL && bytes == 0);
 }
 
+// The sizes by which tests/test_gpu_linear_long.py means to reach each tile, split and not,
+// over more slices than any ring holds.
+static void check_long() {
+  LinPlan p;
+  const struct {
+    int64_t m, k, n;
+    int tile;
+    bool split;
+  } layers[] = {{8200, 1608, 1400, LIN_TILE_256, false},     {1504, 20000, 1504, LIN_TILE_256, true},
+                {4160, 1608, 2304, LIN_TILE_256x192, false}, {2048, 20000, 1032, LIN_TILE_256x192, true},
+                {2000, 1608, 1104, LIN_TILE_128, false},     {520, 20000, 1000, LIN_TILE_128, true},
+                {1500, 1608, 1304, LIN_TILE_64, false},      {257, 30000, 520, LIN_TILE_64, true},
+                {1000, 2312, 760, LIN_TILE_64_DEEP, false},  {64, 6408, 1600, LIN_TILE_64_DEEP, true},
+                {130, 1608, 1000, LIN_TILE_32, false},       {130, 9000, 200, LIN_TILE_32, true},
+                {20, 1608, 16000, LIN_TILE_32_DEEP, false},  {1, 4104, 2304, LIN_TILE_32_DEEP, true},
+                {700, 1001, 1003, LIN_TILE_64_ANY, false},   {257, 30001, 513, LIN_TILE_64_ANY, true}},
+    grads[] = {{3000, 8200, 1400, LIN_TILE_256, false},     {20000, 1400, 2040, LIN_TILE_256, true},
+               {3000, 4160, 2304, LIN_TILE_256x192, false}, {16384, 768, 2304, LIN_TILE_256x192, true},
+               {4000, 2504, 1304, LIN_TILE_128, false},     {3000, 2000, 1104, LIN_TILE_128, true},
+               {4000, 1504, 1304, LIN_TILE_64, false},      {30000, 520, 264, LIN_TILE_64, true},
+               {2004, 333, 2001, LIN_TILE_64_ANY, false},   {3001, 131, 300, LIN_TILE_64_ANY, true}};
+  for (const auto& s : layers) {
+    CHECK(run(layer(s.m, s.k, s.n), &p) == MUON_OK && p.tile == s.tile && p.finish == s.split);
+    CHECK(p.pack.n == 0 && p.gemm.slices >= 8);
+  }
+  for (const auto& s : grads)
+    for (int t : {0, 1}) {  // stored the other way the roles of x and dz change places
+      muon_linear_dw_t l = grad(s.m, t ? s.n : s.k, t ? s.k : s.n);
+      l.dw_transposed = t;
+      l.lddw = t ? l.k : l.n;
+      l.dbias = (float*)at(4);
+      CHECK(run(l, &p) == MUON_OK && p.tile == s.tile && p.finish == s.split);
+      CHECK(p.pack.n == 0 && p.gemm.slices >= 8 && p.gemm.sum_side == 1 + t);
+    }
+  CHECK(run(layer(4097, 1609, 2311), &p) == MUON_OK && p.pack.n == 2 && p.tile == LIN_TILE_256x192);
+  CHECK(run(grad(20001, 1001, 771), &p) == MUON_OK && p.pack.n == 2 && p.finish);
+}
+
 int main() {
+  check_long();
   check_grids();
   check_copies();
   if (g_failures) return 1;

@@ -1,9 +1,10 @@
 """CPU checks of the layer products at the limits of a launch: the host code
-under sanitizers."""
+under sanitizers, and what the inputs of the long GPU tests show."""
 import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -22,3 +23,18 @@ def test_host_code_at_the_limits_of_a_launch(tmp_path):
     assert build.returncode == 0, build.stdout + build.stderr
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.strip() == "ok", run.stdout + run.stderr
+
+
+@pytest.mark.parametrize("k", [1608, 20000])
+def test_a_lost_slice_shows(k):
+    """Values of -1, 0 and 1 (a half, a quarter each): a slice of 64 that is left out, or read in the
+    place of another, changes nearly nine sums in ten.  Its own sum has a variance of
+    64 / 4 and is 0 for 1 in sqrt(2 pi 16) = 10; the difference of two, for 1 in 14."""
+    rng = np.random.default_rng(k)
+    a, b = (rng.integers(0, 4, s).astype(np.float32) for s in ((k, 100), (k, 120)))
+    a, b = (np.where(v < 2, 0, 2 * v - 5) for v in (a, b))
+    whole = a.T @ b
+    lost, stale = slice(k // 128 * 64, k // 128 * 64 + 64), slice(64, 128)
+    without = whole - a[lost].T @ b[lost]
+    assert np.mean(without != whole) > 0.85
+    assert np.mean(without + a[stale].T @ b[stale] != whole) > 0.85
