@@ -391,7 +391,8 @@ typedef struct {
 int muon_linear(const muon_linear_t* layer, void* workspace, size_t workspace_bytes, hipStream_t stream);
 int muon_linear_dx(const muon_linear_t* layer, void* workspace, size_t workspace_bytes, hipStream_t stream);
 /* backward: 0 for muon_linear, 1 for muon_linear_dx.  0 is also given for
- * arguments that the call refuses. */
+ * sizes, types and distances of x and w that the call refuses.  Of pointers only the
+ * alignment of x and w counts; what overlaps is not looked at. */
 size_t muon_linear_workspace_bytes(const muon_linear_t* layer, int backward);
 
 /*

@@ -28,6 +28,7 @@ struct Matrix {
 
   uintptr_t lo() const { return (uintptr_t)p; }
   uint64_t size() const { return grad_type_bytes(type); }
+  int64_t pitch() const { return rows == 1 ? cols : ld; }  // that of one row is not given
   uintptr_t hi() const { return lo() + (uint64_t)((rows - 1) * ld + cols) * size(); }
   bool is(const Matrix& o) const { return p == o.p && type == o.type && (ld == o.ld || rows == 1); }
 };
@@ -38,11 +39,11 @@ int check_dim(int64_t v, int64_t least, int64_t most, const char* what) {
   return MUON_OK;
 }
 
-int check_matrix(const Matrix& m) {
+int check_matrix(const Matrix& m, bool sizes_only = false) {
   if (m.type < MUON_FP32 || m.type > MUON_FP16)
     return fail(MUON_EINVAL, "%s: type %d is no element type (MUON_FP32, MUON_BF16, MUON_FP16)", m.what, m.type);
-  if (!m.p) return fail(MUON_EINVAL, "%s is NULL", m.what);
-  if (m.lo() % m.size()) return fail(MUON_EINVAL, "%s is not %d-byte aligned", m.what, (int)m.size());
+  if (!m.p && !sizes_only) return fail(MUON_EINVAL, "%s is NULL", m.what);
+  if (m.lo() % m.size() && !sizes_only) return fail(MUON_EINVAL, "%s is not %d-byte aligned", m.what, (int)m.size());
   if (m.rows > 1 && (m.written ? m.ld < m.cols : m.ld < 0))
     return fail(MUON_EINVAL, "%s: rows %lld elements apart%s", m.what, (long long)m.ld,
                 m.written ? " overlap" : "");
@@ -106,14 +107,11 @@ char* take(LinPlan* p, void* workspace, size_t bytes) {
 
 // The operand that the kernels read for m, through a copy where they must.
 LinOperand operand_of(const Matrix& m, int type, LinPlan* plan, void* workspace) {
-  if (plan->tile == LIN_TILE_64_ANY) return {m.p, m.ld * (int64_t)m.size(), 0};
-  if (readable(m, type)) {
-    const int64_t ld = m.rows == 1 ? m.cols : m.ld;
-    return {m.p, ld * 2, ((m.rows - 1) * ld + m.cols) * 2};
-  }
+  if (plan->tile == LIN_TILE_64_ANY) return {m.p, m.pitch() * (int64_t)m.size(), 0};
+  if (readable(m, type)) return {m.p, m.pitch() * 2, ((m.rows - 1) * m.pitch() + m.cols) * 2};
   const int64_t ld = (m.cols + 7) / 8 * 8;
   char* dst = take(plan, workspace, (size_t)(m.rows * ld * 2));
-  plan->pack.job[plan->pack.n++] = {m.p, dst, m.ld, ld, m.rows, m.cols, m.type, type};
+  plan->pack.job[plan->pack.n++] = {m.p, dst, m.pitch(), ld, m.rows, m.cols, m.type, type};
   return {dst, ld * 2, m.rows * ld * 2};
 }
 
@@ -158,7 +156,7 @@ struct Copies {
     for (const Matrix* m : {&a, &b}) {
       if (m->rows == 0) return;
       if (!readable(*m, type)) us += (double)(m->rows * m->cols) * (double)(m->size() + 2) / 4e6;
-      unaligned = unaligned || m->lo() % 16 != 0 || m->ld * (int64_t)m->size() % 16 != 0;
+      unaligned = unaligned || m->lo() % 16 != 0 || m->pitch() * (int64_t)m->size() % 16 != 0;
     }
     if (us == 0) return;
     us += 3.0;
@@ -215,7 +213,8 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies
   return MUON_OK;
 }
 
-// sizes_only: pointers may be anything (the size of the workspace is asked for).
+// sizes_only: pointers may be anything (the size of the workspace is asked for), and only
+// the distances that its size goes by are checked.
 int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool sizes_only, LinPlan* p) {
   *p = LinPlan{};
   int rc;
@@ -244,7 +243,9 @@ int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool size
   const Matrix x = {"x", l->x, l->m, in, l->ldx, type, false};
   const int64_t w_rows = l->w_transposed ? l->n : l->k, w_cols = l->w_transposed ? l->k : l->n;
   const Matrix w = {"w", l->w, w_rows, w_cols, l->ldw, l->w_type, false};
-  if (!sizes_only) {
+  if (sizes_only) {
+    if ((rc = check_matrix(x, true)) || (rc = check_matrix(w, true))) return rc;
+  } else {
     Matrix all[6] = {y, x, w};
     bool may_be_y[6] = {};
     int n = 3;
@@ -322,7 +323,9 @@ int plan_grad(const muon_linear_dw_t* l, void* workspace, bool sizes_only, LinPl
   const Matrix dw = {"dw", l->dw, rows, cols, l->lddw, MUON_FP32, true};
   const Matrix x = {"x", l->x, l->m, l->k, l->ldx, type, false};
   const Matrix dz = {"dz", l->dz, l->m, l->n, l->lddz, type, false};
-  if (!sizes_only) {
+  if (sizes_only) {
+    if (l->m > 0 && ((rc = check_matrix(x, true)) || (rc = check_matrix(dz, true)))) return rc;
+  } else {
     Matrix all[4] = {dw};
     const bool none[4] = {};
     int n = 1;

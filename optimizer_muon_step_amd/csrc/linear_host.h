@@ -36,7 +36,7 @@ int plan_linear_dw(const muon_linear_dw_t* l, void* workspace, size_t workspace_
 // Blocks of the launch in *blocks, 0 where there is nothing to do.
 int plan_dropout(const muon_dropout_t* d, DropArgs* out, int64_t* blocks);
 
-// Bytes of workspace, without the checks of pointers.
+// Bytes of workspace; checks sizes, types and the distances of what is read, not pointers.
 int linear_workspace(const muon_linear_t* l, bool backward, size_t* bytes);
 int linear_dw_workspace(const muon_linear_dw_t* l, size_t* bytes);
 

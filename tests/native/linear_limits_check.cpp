@@ -3,6 +3,7 @@
 // over for others, and copies of more blocks than a launch has go out in several.  Built and run by tests/test_linear_limits.py, under
 // sanitizers.  Prints "ok" and exits 0 when every check holds.
 #include <cstdio>
+#include <limits>
 #include <string>
 #include <vector>
 
@@ -175,7 +176,63 @@ static void check_long() {
   CHECK(run(grad(20001, 1001, 771), &p) == MUON_OK && p.pack.n == 2 && p.finish);
 }
 
+// The distance between rows of a matrix of one row means nothing, whatever it is.
+static void check_one_row() {
+  const int64_t any[] = {0, 3, -1, std::numeric_limits<int64_t>::max(), std::numeric_limits<int64_t>::min()};
+  for (int64_t k : {1, 8, 61, 768})
+    for (int64_t n : {1, 61, 768, 6400})
+      for (int type : {MUON_BF16, MUON_FP32}) {
+        muon_linear_t l = layer(1, k, n);
+        l.w_type = type;
+        l.preact = at(4);
+        l.residual = at(5);
+        l.ldp = l.ldr = n;
+        LinPlan want, p;
+        CHECK(run(l, &want) == MUON_OK);
+        for (int64_t ld : any) {
+          l.ldx = l.ldy = l.ldp = l.ldr = ld;
+          if (k == 1) l.ldw = ld;
+          CHECK(run(l, &p) == MUON_OK && p.tile == want.tile && p.gemm.splits == want.gemm.splits);
+          CHECK(p.gemm.a.ld == want.gemm.a.ld && p.gemm.b.ld == want.gemm.b.ld && p.workspace == want.workspace);
+        }
+        muon_linear_dw_t g = grad(1, k, n);
+        CHECK(run(g, &want) == MUON_OK);
+        for (int64_t ld : any) {
+          g.ldx = g.lddz = ld;
+          if (k == 1) g.lddw = ld;
+          CHECK(run(g, &p) == MUON_OK && p.tile == want.tile && p.gemm.a.ld == want.gemm.a.ld && p.gemm.b.ld == want.gemm.b.ld);
+        }
+      }
+}
+
+// The size of a workspace is asked for before there are buffers: pointers may be anything,
+// the distances of what is read not.
+static void check_sizes() {
+  for (int64_t ld : {std::numeric_limits<int64_t>::max(), std::numeric_limits<int64_t>::min(), (int64_t)-1, (int64_t)1 << 60}) {
+    size_t bytes = 1;
+    muon_linear_t l = layer(64, 61, 64);
+    l.x = l.w = l.y = nullptr;
+    l.ldx = ld;
+    CHECK(linear_workspace(&l, false, &bytes) == MUON_EINVAL && bytes == 0);
+    l.ldx = 61;
+    l.ldw = ld;
+    CHECK(linear_workspace(&l, true, &bytes) == MUON_EINVAL && bytes == 0);
+    l.ldw = 64;
+    l.ldy = ld;  // the size does not go by it
+    CHECK(linear_workspace(&l, false, &bytes) == MUON_OK);
+    muon_linear_dw_t g = grad(64, 61, 64);
+    g.x = g.dz = nullptr;
+    g.dw = nullptr;
+    g.lddz = ld;
+    CHECK(linear_dw_workspace(&g, &bytes) == MUON_EINVAL && bytes == 0);
+    g.lddz = 64;
+    CHECK(linear_dw_workspace(&g, &bytes) == MUON_OK);
+  }
+}
+
 int main() {
+  check_sizes();
+  check_one_row();
   check_long();
   check_grids();
   check_copies();
