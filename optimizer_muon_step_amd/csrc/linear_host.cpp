@@ -184,13 +184,17 @@ int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies
     // few rows of a weight, or few weights over few rows, are no case worth a kernel
     if (grad && (tile == LIN_TILE_32 || tile == LIN_TILE_64_DEEP || tile == LIN_TILE_32_DEEP)) continue;
     if (tile == LIN_TILE_64_ANY && !copies.avoidable) continue;
-    // up to 32 rows the whole LDS serves one tile better: one row of 2304 over 768
-    // takes 7.5 us in it, 5.4 with the deep ring, 5.9 in 64 x 64 with its own
-    if (tile == LIN_TILE_32 && m <= 32) continue;
     const bool any = tile == LIN_TILE_64_ANY;
     const double slower = (grad && tile != LIN_TILE_256x192 ? GRAD_SLICE : 1.0) * (any && copies.unaligned ? UNALIGNED_SLICE : 1.0);
     const LinTileSize t = kLinTile[tile];
     const int64_t tm = (m + t.bm - 1) / t.bm, tn = (n + t.bn - 1) / t.bn, tiles = tm * tn;
+    // Up to 32 rows take 32 x 64 tiles with either ring, which cost the same while every tile has a unit to
+    // itself; the deep one is taken there.  One row of 2304 over 768, 1600 and 3072, the weight's rows
+    // along K: read from HBM 5.8, 8.8 and 13.1 us with the deep ring, 5.8, 8.8 and 13.3 with the other;
+    // from the caches 5.5, 8.4 and 12.8, and 5.3, 8.0 and 12.3.  Beyond, the other fits twice into a unit:
+    // one row of 50257 over 768, from HBM (from the caches), 19.2 us (16.1) with it, 24.3 (21.9) with the
+    // deep ring, 21.2 (16.7) in 64 x 64; of 20000 10.6 (9.2), 13.3 (12.2) and 11.4 (9.0).
+    if (tile == LIN_TILE_32 && m <= 32 && tiles <= 256) continue;
     const int slices = ceil_div(k, t.bk);
     for (int fill = 0; fill <= 2; ++fill) {  // no splits, or as many as make one or two rounds
       const int64_t want = fill == 0 ? 1 : std::min<int64_t>(256 * fill / tiles, slices * t.bk / 256);

@@ -230,7 +230,22 @@ static void check_sizes() {
   }
 }
 
+// Up to 32 rows: the deep ring while every tile has a unit to itself, two tiles to a unit beyond.
+static void check_few_rows() {
+  LinPlan p;
+  for (int64_t m : {1, 8, 32}) {
+    CHECK(run(layer(m, 768, 16384), &p) == MUON_OK && p.tile == LIN_TILE_32_DEEP && p.gemm.tiles_n == 256);
+    for (int64_t n : {16392, 20000, 32768, 50264, 100000})
+      CHECK(run(layer(m, 768, n), &p) == MUON_OK && p.tile == LIN_TILE_32 && p.gemm.tiles_n > 256);
+    muon_linear_t l = layer(m, 768, 50257);  // a vocabulary of the framework's, stored out x in
+    l.w_transposed = 1;
+    l.ldw = 768;
+    CHECK(run(l, &p) == MUON_OK && p.tile == LIN_TILE_32 && p.pack.n == 0);
+  }
+}
+
 int main() {
+  check_few_rows();
   check_sizes();
   check_one_row();
   check_long();

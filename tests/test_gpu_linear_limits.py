@@ -61,3 +61,17 @@ def test_more_tiles_than_a_launch():
     assert y.shape == (m, n)
     for a in range(0, m, step):
         assert torch.equal(y[a:a + step].float(), x[a:a + step].float() @ w.float()), a
+
+
+@pytest.mark.parametrize("order", ["rows", "columns"])
+@pytest.mark.parametrize("m,n", [(1, 20000), (32, 50264), (5, 16392), (1, 50257)])
+def test_few_rows_of_many_columns(m, n, order):
+    """More tiles than compute units: two to a unit."""
+    torch = torch_mod()
+    import optimizer_muon_step_amd as mu
+    k = 768
+    x, w = signs((m, k), "bf16", 6), signs((k, n), "bf16", 7) if order == "rows" else signs((n, k), "bf16", 7).T
+    bias = signs((n,), "bf16", 8)
+    want = (x.double() @ w.double()).float() + bias.float()
+    assert torch.equal(mu.muon_linear(x, w, bias=bias, out_dtype=torch.float32), want)
+    assert torch.equal(mu.muon_linear_dx(x, w.T, residual=bias.expand(m, n)), want.bfloat16())
