@@ -15,7 +15,6 @@ namespace lin {
 
 using grad::f32x4;
 using grad::f32x4_u;
-using grad::u16x8_u;
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));

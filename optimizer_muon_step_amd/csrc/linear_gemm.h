@@ -73,11 +73,10 @@ __device__ __forceinline__ void block_barrier() {
 // 16 bytes a lane from a buffer to LDS at `to` + 16 lane.  Written out, since
 // before every LDS read the compiler would wait for all of its own such loads,
 // those of later slices among them; the waits are wait_loads'.  It has no
-// result in registers, and nothing else in these kernels uses M0.  M0 has to be
-// set one wait state ahead, and a descriptor that a vector instruction left (a
-// spilled scalar's way back, too) five.
+// result in vector registers.  M0 has to be set one wait state ahead, and a
+// descriptor that a vector instruction left (a spilled scalar's way back, too) five.
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t to, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(rsrc) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(rsrc) : "m0", "memory");
 }
 
 template <int TYPE>
