@@ -330,6 +330,9 @@ int muon_step_clip(float* const* params, const float* const* grads, float* const
  *           16 (c mod 8) and up.  The mask is never stored: muon_linear_dx and
  *           muon_dropout make it anew from the same numbers, for a matrix of the
  *           same width.  site tells a model's dropouts apart, step the training steps.
+ *           r counts the rows of the call: calls that take other rows of one batch
+ *           (micro-batches, ranks) need a step or seed of their own, or they drop the
+ *           same places.
  *
  * Fields of muon_linear_t (for muon_linear_dx x is dz, m x n, y is dx, m x k,
  * residual is m x k and preact, read, m x k):

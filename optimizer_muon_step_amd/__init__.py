@@ -415,7 +415,8 @@ def muon_linear(x, w, bias=None, act=None, dropout=0.0, rng=None, site=0, residu
     (seed, step), or an int64 tensor of the two on the GPU, read when the call
     runs (under a captured graph: at every replay); `site` tells the dropouts of
     a model apart.  The mask is never stored: the same dropout, rng and site in
-    muon_linear_dx or muon_dropout, on a matrix as wide, make it again.
+    muon_linear_dx or muon_dropout, on a matrix as wide, make it again.  It goes by
+    the row within the call: micro-batches and ranks need a step or seed of their own.
     `residual` and the result are of x's type or float32 (`out_dtype`; by default the
     residual's type, or x's); `out` is a tensor to fill, and may be the residual.
     `preact`, of x's type, receives x w + bias for the backward pass.  Rows may
