@@ -321,6 +321,8 @@ int muon_step_clip(float* const* params, const float* const* grads, float* const
  * dbias are fp32.  Equal calls give equal bits.
  *   act     MUON_ACT_GELU  z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3)
  *           MUON_ACT_RELU  max(z, 0);  MUON_ACT_RELU2  max(z, 0)^2
+ *           act' of relu is 0 for z <= 0 and 1 above, of relu2 2 max(z, 0).  A NaN z
+ *           has a NaN act and act', in every activation
  *   drop    with t = min(65535, floor(2^16 dropout + 1/2)): an element whose 16 random
  *           bits are at least t is kept, times 2^16 / (2^16 - t); the others become 0,
  *           whatever they were (an infinity or NaN too).  So `dropout` acts in steps

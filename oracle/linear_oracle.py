@@ -18,6 +18,8 @@ Readings taken where the pages are silent:
   L3 mask         16 bits an element; kept where they are >= t = floor(2^16 p +
                   1/2), at most 65535, and then times 2^16 / (2^16 - t); p is
                   the fp32 value of the argument
+  L4 NaN          act and act' of a NaN are NaN, in every activation; a dropped
+                  element is 0 whatever it was
 """
 
 from __future__ import annotations
@@ -88,9 +90,9 @@ def slope(z, kind):
         gate, rest = gate_of(z)
         return gate + z * gate * rest * 2.0 * C * (1.0 + 3 * 0.044715 * z * z)
     if kind == "relu":
-        return np.where(z > 0, 1.0, 0.0)
+        return np.where(z <= 0, 0.0, np.where(z > 0, 1.0, z))
     if kind == "relu2":
-        return np.where(z > 0, 2.0 * z, 0.0)
+        return np.where(z <= 0, 0.0, 2.0 * z)
     return np.ones_like(z)
 
 

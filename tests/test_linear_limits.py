@@ -1,11 +1,14 @@
 """CPU checks of the layer products at the limits of a launch: the host code
-under sanitizers, and what the inputs of the long GPU tests show."""
+under sanitizers, what the inputs of the long GPU tests show, and the oracle at
+special values."""
 import os
 import shutil
 import subprocess
 
 import numpy as np
 import pytest
+
+from oracle import linear_oracle as lo
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "optimizer_muon_step_amd", "csrc")
@@ -38,3 +41,14 @@ def test_a_lost_slice_shows(k):
     without = whole - a[lost].T @ b[lost]
     assert np.mean(without != whole) > 0.85
     assert np.mean(without + a[stale].T @ b[stale] != whole) > 0.85
+
+
+def test_oracle_at_special_values():
+    """act and act' of a NaN are NaN; relu's and relu2's slope at zeros and infinities."""
+    nan, inf = float("nan"), float("inf")
+    for kind in ("gelu", "relu", "relu2"):
+        assert np.isnan(lo.act(np.array([nan]), kind)).all() and np.isnan(lo.slope(np.array([nan]), kind)).all()
+    z = np.array([0.0, -0.0, 3.0, -3.0, inf, -inf])
+    assert lo.slope(z, "relu").tolist() == [0, 0, 1, 0, 1, 0] and lo.slope(z, "relu2").tolist() == [0, 0, 6, 0, inf, 0]
+    # a dropped element does not see it
+    assert lo.through(np.ones(2), "relu", np.array([nan, nan]), np.array([0.0, 2.0])).tolist()[0] == 0
