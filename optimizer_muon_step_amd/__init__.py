@@ -422,7 +422,9 @@ def muon_linear(x, w, bias=None, act=None, dropout=0.0, rng=None, site=0, residu
     `preact`, of x's type, receives x w + bias for the backward pass.  Rows may
     lie apart in memory and start anywhere; the fastest kernels take rows
     that are 16-byte aligned and multiples of 8 elements long, and large products copy
-    others (and float32 weights) first.  `stream` as in muon_grad_norm.  No autograd graph is recorded."""
+    others (and float32 weights) first.  `stream` as in muon_grad_norm.  No autograd graph is
+    recorded, whatever requires a gradient: muon_linear_dx, muon_linear_dw and muon_dropout are the
+    backward pass."""
     return _linear(x, w, bias, act, dropout, rng, site, residual, out, out_dtype, preact, 0, stream)
 
 
@@ -434,7 +436,8 @@ def muon_linear_dx(dz, w, act=None, preact=None, dropout=0.0, rng=None, site=0, 
     `act` and `preact` (both or neither), `dropout`, `rng` and `site` are those of the
     layer whose output x is, so that the result is the gradient of that layer's z;
     `residual` is a gradient that reaches x another way.  Types, memory
-    orders, `out` (which may be the residual or preact) and `stream` as in muon_linear."""
+    orders, `out` (which may be the residual or preact) and `stream` as in muon_linear.
+    No autograd graph is recorded."""
     return _linear(dz, w, None, act, dropout, rng, site, residual, out, out_dtype, preact, 1, stream)
 
 
@@ -453,7 +456,8 @@ def muon_linear_dw(x, dz, dw, dbias=None, accumulate=False, stream=None) -> None
     dz over its rows, or both added to what the tensors hold (`accumulate`: the
     micro-batches of a step).  `x` and `dz` are bfloat16 or float16, (..., inputs) and
     (..., outputs); `dw` is float32, inputs x outputs in either memory order,
-    as muon_step reads it, and `dbias` float32, as muon_adamw_step does."""
+    as muon_step reads it, and `dbias` float32, as muon_adamw_step does.  No autograd
+    graph is recorded; autograd takes what is written as changed.  `stream` as in muon_grad_norm."""
     if stream is not None:
         with _on_stream(stream):
             return muon_linear_dw(x, dz, dw, dbias, accumulate)
@@ -465,7 +469,8 @@ def muon_dropout(x, p, rng, site=0, act=None, preact=None, residual=None, out=No
     gradient (the same call on the gradient), or with `act` and `preact` the gradient dz of a
     layer's z behind activation and dropout.  float32, bfloat16 or float16; the
     mask goes by the last dimension and the rows before it, as in muon_linear.
-    `out` may be x, preact or residual."""
+    `out` may be x, preact or residual.  No autograd graph is recorded.  `stream` as in
+    muon_grad_norm."""
     if stream is not None:
         with _on_stream(stream):
             return muon_dropout(x, p, rng, site, act, preact, residual, out, out_dtype)

@@ -1,4 +1,5 @@
-"""CPU checks of the streams that the layer products and dropout take."""
+"""CPU checks of the streams that the layer products and dropout take, and of
+what their documentation says of streams and autograd."""
 import pytest
 
 
@@ -25,3 +26,10 @@ def test_the_per_thread_stream_is_refused(monkeypatch):
     for call in calls:  # another stream: what is wrong is that the tensors are on the CPU
         with pytest.raises(ValueError, match="on the GPU"):
             call()
+
+
+def test_the_documentation_names_streams_and_autograd():
+    import optimizer_muon_step_amd as mu
+    for call in (mu.muon_linear, mu.muon_linear_dx, mu.muon_linear_dw, mu.muon_dropout):
+        text = " ".join(call.__doc__.split())
+        assert "No autograd graph is recorded" in text and "`stream`" in text, call.__name__
