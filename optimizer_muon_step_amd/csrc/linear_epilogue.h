@@ -81,24 +81,15 @@ __device__ __forceinline__ f32x8 sum_of_parts(const float* at, int64_t stride, i
   return v;
 }
 
-// stream: past the caches.
 template <int TYPE>
-__device__ __forceinline__ void store8(void* p, int64_t i, f32x8 v, bool stream = false) {
+__device__ __forceinline__ void store8(void* p, int64_t i, f32x8 v) {
   MUON_GLOBAL typename grad::Elem<TYPE>::scalar* s = gptr(static_cast<typename grad::Elem<TYPE>::scalar*>(p)) + i;
   if constexpr (TYPE == GRAD_FP32) {
-    const f32x4_u lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-    if (stream) {
-      __builtin_nontemporal_store(lo, reinterpret_cast<MUON_GLOBAL f32x4_u*>(s));
-      __builtin_nontemporal_store(hi, reinterpret_cast<MUON_GLOBAL f32x4_u*>(s + 4));
-    } else {
-      *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s) = lo;
-      *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s + 4) = hi;
-    }
+    *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s) = f32x4_u{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<MUON_GLOBAL f32x4_u*>(s + 4) = f32x4_u{v[4], v[5], v[6], v[7]};
   } else {
     const u32x4 w = narrow8<TYPE>(v);
-    const u32x4_u u = {w.x, w.y, w.z, w.w};
-    if (stream) __builtin_nontemporal_store(u, reinterpret_cast<MUON_GLOBAL u32x4_u*>(s));
-    else *reinterpret_cast<MUON_GLOBAL u32x4_u*>(s) = u;
+    *reinterpret_cast<MUON_GLOBAL u32x4_u*>(s) = u32x4_u{w.x, w.y, w.z, w.w};
   }
 }
 template <int TYPE>

@@ -337,7 +337,7 @@ struct LayerStore {
   __device__ __forceinline__ void put(int d, f32x8 v, const Fetched& f) const {
     if constexpr (!BACKWARD) {
       v += bias;
-      if (e.preact) store8<TYPE>(e.preact, at_p + d * e.ldp, v, e.stream);
+      if (e.preact) store8<TYPE>(e.preact, at_p + d * e.ldp, v);
       v = act8<ACT>(v);
     } else if constexpr (SLOPE) {
       v = slope8<ACT>(widen8<TYPE>(f.z)) * v;
@@ -346,9 +346,9 @@ struct LayerStore {
     if constexpr (RES) v = widen8<TYPE>(f.r) + v;
     if (!RES && wide) {
       if (e.residual) v = load8<GRAD_FP32>(e.residual, at_r + d * e.ldr) + v;
-      store8<GRAD_FP32>(e.y, at_y + d * e.ldy, v, e.stream);
+      store8<GRAD_FP32>(e.y, at_y + d * e.ldy, v);
     } else {
-      store8<TYPE>(e.y, at_y + d * e.ldy, v, e.stream);
+      store8<TYPE>(e.y, at_y + d * e.ldy, v);
     }
   }
 };

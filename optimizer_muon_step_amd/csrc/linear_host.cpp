@@ -291,10 +291,6 @@ int plan_layer(const muon_linear_t* l, bool backward, void* workspace, bool size
   e.act = l->act;
   e.backward = backward;
   fill_dropout(&e, l->dropout, l->seed, l->step, l->site, l->rng);
-  // What does not stay in the memory-side cache (256 MiB) until it is read goes
-  // past the caches: 32768 x 6400 y and z over 1600 712 us so and 755 us through
-  // them; 16384 x 3072 over 768, which does stay, 105 and 102.
-  e.stream = l->m * out * ((l->y_type == MUON_FP32 ? 4 : 2) + (l->preact && !backward ? 2 : 0)) > ((int64_t)256 << 20);
   if (g.splits > 1) {
     const LinTileSize t = kLinTile[p->tile];
     LinJoinArgs& j = p->join;

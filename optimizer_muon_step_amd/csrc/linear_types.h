@@ -35,7 +35,6 @@ struct LinEpilogue {
   int32_t bias_type, y_type;
   int32_t act;
   int32_t backward;
-  int32_t stream;  // what is written goes past the caches
 };
 
 // An operand as the products read it: 16-bit elements, 16-byte aligned, rows of
