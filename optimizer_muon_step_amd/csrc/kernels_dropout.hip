@@ -58,8 +58,9 @@ __device__ __forceinline__ f32x8 load_some(const void* p, int64_t i, int have) {
 }
 
 // y = residual + drop(x) act'(preact), an eight to a thread: 16384 x 768 bf16 with a
-// residual 13.6 us (5.5 TB/s; the generator's 7 rounds hide behind the loads), with
-// two 14.0 and with four 15.5; loads or stores past the caches gained nothing.
+// residual 13.6 us where three sets of operands, 226 MB, change places in the 256 MiB memory-side
+// cache (5.5 TB/s; the generator's 7 rounds hide behind the loads), with two 14.0 and with four 15.5;
+// 17.4 us (4.3 TB/s) where 12 sets leave nothing in it.  Loads or stores past the caches gained nothing.
 template <int XT, int YT, int ACT>
 __global__ __launch_bounds__(DROP_THREADS) void dropout_kernel(const DropArgs a) {
   const LinEpilogue& e = a.e;

@@ -29,8 +29,9 @@ hipError_t launch_linear_dw(const LinGemmArgs& a, int type, int tile, hipStream_
 
 // A thread to eight elements of a row of c, and behind them a block to 32 of the
 // sums, whose many rows its 8 groups of threads share.  Everything is added in an order
-// that the sizes give, so equal calls give equal bits.  HBM-bound: 5 splits of 768 x 3072
-// added to c, 66 MB, 11.8 us (5.6 TB/s).
+// that the sizes give, so equal calls give equal bits.  Memory-bound: 5 splits of 768 x 3072
+// added to c, 66 MB, 11.8 us (5.6 TB/s, more than HBM's 5.1: the launch before has just written
+// the 47 MB of parts, which the memory-side cache holds).
 __global__ __launch_bounds__(FINISH_THREADS) void linear_finish_kernel(const LinFinishArgs a) {
   if ((int)blockIdx.x >= a.sum_first_block) {
     constexpr int GROUPS = FINISH_THREADS / FINISH_SUMS;

@@ -25,10 +25,11 @@
 //
 // Measured (bf16, one MI355X): 16384 x 3072 over 768 with GELU and z kept 102 us, 760
 // TFLOP/s, 65 us of it the main loop and the rest 200 MB of stores that a round of tiles
-// ends with; 32768 x 6400 over 1600 690 us, 970 TFLOP/s, matrix cores busy 43 %: with 256 x 256 tiles
+// ends with; 32768 x 6400 over 1600, likewise, 690 us, 970 TFLOP/s, matrix cores busy 43 %: with 256 x 256 tiles
 // of 8 waves LDS reads and barriers take their turns beside them (at 8192^3 540 us of matrix instructions alone, 612
 // with the reads, 630 with barriers, 800 with the loads).  16384 x 768 over
-// 3072 is 256 tiles of 256 x 192, one to a compute unit: 82 us with dropout and residual. One row is latency, 5.4 us.
+// 3072 is 256 tiles of 256 x 192, one to a compute unit: 81 us with dropout and residual.  One row of
+// 2304 over 768 is latency, 5.4 us.
 #pragma once
 
 #include <hip/hip_runtime.h>

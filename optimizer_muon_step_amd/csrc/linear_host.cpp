@@ -141,9 +141,10 @@ double tiles_us(int tile, int64_t tiles, double slices) {
 }
 
 // A split leaves its sums in memory and a last pass adds them up: 3 us for the
-// launch, and the sums written and read at 5 TB/s.  For a layer of few rows (us, with and
-// without splits): 1 x 768 over 3072 6.8 and 12.0, 64 x 1600 over 6400 11.8 and
-// 20.9, 2048 x 1600 over 6400 57 and 70; 1 x 2304 over 768 is not split, 5.4.
+// launch, and the sums written and read at 5 TB/s.  For a layer of few rows with a bias (us in a graph,
+// three sets of operands in turn, with and without splits): 1 x 768 over 3072 7.0 and 12.6,
+// 64 x 1600 over 6400 13.2 and 22.1, 2048 x 1600 over 6400 62 and 71 (one set: 57 and 70);
+// 1 x 2304 over 768 is not split, 5.4.
 double splits_us(int64_t m, int64_t n, int64_t splits) { return splits == 1 ? 0 : 3.0 + (double)(m * n * splits) * 8 / 5e6; }
 
 // The copies that operands need in all tiles but 64_ANY: 3 us for the launch, their
@@ -165,15 +166,18 @@ struct Copies {
 };
 
 // Tiles, slices and splits of a product: what the measured times make the
-// fastest.  Examples (us, chosen and next): 16384 x 3072 over 768 90 in 256 x 256
-// tiles, 101 in 256 x 192; 16384 x 768 over 3072 67 in 256 x 192 (256 tiles, one to a unit), 79 in
-// 256 x 256; 4096 x 768 over 768 12.2 in 128 x 128, 19.1 in 256 x 192;
-// 1024 x 768 over 2304 11.4 in 64 x 64 with the deep ring, 12.6 with the other, 28
-// in 128 x 128; 512 x 768 over 3072 12.2 in 32 x 64, 13.4 in 64 x 64.
+// fastest.  The times leave the epilogue out, whose loads and stores cost all tiles about the same.
+// Examples (us, forward with a bias, bf16, in a graph, three sets of operands in turn; chosen and next):
+// 16384 x 3072 over 768 85 in 256 x 256 tiles, 92 in 256 x 192 (with GELU 94 and 102, with z
+// kept too 103 and 112); 16384 x 768 over 3072 78 in 256 x 192 (256 tiles, one to a unit), 87 in
+// 256 x 256 (with dropout and residual 83 and 91); 4096 x 768 over 768 12.9 in 128 x 128, 19.6 in 256 x 192;
+// 1024 x 768 over 2304 11.5 in 64 x 64 with the deep ring, 14.7 with the other, 20
+// in 128 x 128; 512 x 768 over 3072 12.5 in 32 x 64, 15.6 in 64 x 64.
 //
-// 64_ANY stands against the copies and any other tile: 1 x 2304 over 768 of an fp32 weight
-// 6.8 us in it and 9.6 with the copy, 1999 x 771 over 1001 16.3 and 18.8; 4096 x 768
-// over 768 of an fp32 weight 17.0 and 16.1, 16384 x 3072 235 and 99.
+// 64_ANY stands against the copies and any other tile.  Of an fp32 weight (the same form): 1 x 2304
+// over 768 6.9 us in it and 9.3 with the copy, 4096 x 768 over 768 18.5 and 16.3, 16384 x 3072
+// over 768 231 and 87.  1999 x 771 over 1001, fp16: 18.8 and 20.7, of an fp32 weight 20.2 and
+// 20.0, where the copy's launch and workspace cost a call 4 us on the host besides.
 int lay_out(LinPlan* p, int64_t m, int64_t n, int64_t k, bool grad, const Copies& copies) {
   LinGemmArgs& g = p->gemm;
   g.m = (int32_t)m;
